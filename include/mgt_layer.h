@@ -243,6 +243,103 @@ mgt_status mgt_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* A, int64
                         const float* b_scales, void* C, int32_t c_dtype, int64_t ldc,
                         int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Microscaled 4-bit floating point. The vampireachao.github.io page lists FP4 among Megatron
+ * Core's mixed precisions, without a recipe; the formats here are the two that the tensor cores
+ * of sm_100a scale themselves.
+ *
+ * Elements are e2m1: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, rounded to nearest, ties to even,
+ * saturating at +-6. Blocks run along the columns of an operand, the axis that a product sums:
+ *   MGT_MXFP4  32 elements share 2^e, e = floor(log2(amax)) - 2 and at least -127, held as the
+ *              byte e + 127 (0 for a block of zeros; 255, NaN, for a block that holds an infinity
+ *              or a NaN, with zero codes). OCP Microscaling Formats, version 1.0.
+ *   MGT_NVFP4  16 elements share s = e4m3(amax / (6 f)), rounded to nearest even and saturating
+ *              at 448 (0x7f, NaN, as above), and the tensor shares the factor f: an element
+ *              stands for e2m1 * s * f. mgt_mx4_tensor_factor gives f; a kept one (a calibrated
+ *              scale) may be any positive number, and a power of two keeps every rounding
+ *              decision exact.
+ *
+ * mgt_mx4: one operand of `rows` by `cols`.
+ *   codes    rows of ld / 2 bytes, two elements to a byte, the even column in the low half.
+ *            Columns from cols up to the next multiple of 128 hold zeros.
+ *   scales   tiles of 128 rows by 4 blocks, 512 bytes each, row r and block b at byte
+ *            16 (r % 32) + 4 (r % 128 / 32) + b % 4 of tile (r / 128) * (ld / (4 * block)) + b / 4:
+ *            the order in which the tensor core takes them. Whole tiles of rows; those behind
+ *            the last row are not read into any result and not written.
+ *   ld       leading dimension in elements, a multiple of 128, at least cols rounded up to it. An
+ *            operand may be a part of a wider one that starts at a row and column that are
+ *            multiples of 128: codes + (row * ld + col) / 2, scales + 512 * (row / 128 *
+ *            (ld / (4 * block)) + col / (4 * block)).
+ *   factor   MGT_NVFP4: device pointer to two floats {amax, f}; only f is read. Else unused.
+ * codes and scales are 16-byte aligned. mgt_mx4_sizes gives ld and the bytes of both buffers for
+ * an operand of its own.
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, keep nothing and check their arguments
+ * before they launch (MGT_EINVAL for shapes that do not fit together and missing pointers,
+ * MGT_EUNSUPPORTED for types and alignments). Outputs may not overlap inputs. Results do not
+ * depend on timing or order. They may be captured into a graph. */
+typedef enum mgt_mx4_format { MGT_MXFP4 = 0, MGT_NVFP4 = 1 } mgt_mx4_format;
+typedef enum mgt_act { MGT_ACT_SILU = 0, MGT_ACT_GELU = 1, MGT_ACT_GELU_TANH = 2 } mgt_act;
+
+typedef struct mgt_mx4 {
+  int32_t format; /* mgt_mx4_format */
+  int32_t rows, cols;
+  int64_t ld;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* factor;
+} mgt_mx4;
+
+mgt_status mgt_mx4_sizes(int32_t format, int32_t rows, int32_t cols, int64_t* ld,
+                         size_t* code_bytes, size_t* scale_bytes);
+
+/* factor = {amax, f} of x [rows][cols] (row stride ldx elements; dtype MGT_F32 or MGT_BF16): amax
+ * over the finite elements, f = 2^ceil(log2(amax / 2688)), at least 2^-126, 1 where amax is 0
+ * (2688 = 6 * 448, the largest element times the largest scale). */
+mgt_status mgt_mx4_tensor_factor(int32_t dtype, int32_t rows, int32_t cols, const void* x,
+                                 int64_t ldx, float* factor, void* stream);
+
+/* Quantise x into q ([rows][cols], blocks along a row of x) and / or qt ([cols][rows], x
+ * transposed, blocks along a column of x): either may be NULL. Both are made from one read, and in
+ * MGT_NVFP4 then share one factor pointer. Gradients of a product need both: with Q(.) for
+ * quantisation along the summed axis and y = Q(x) Q(W)^T, dx = Q(dy) Q(W^T)^T and
+ * dW = Q(dy^T) Q(x^T)^T. */
+mgt_status mgt_mx4_quantize(int32_t dtype, const void* x, int64_t ldx, const mgt_mx4* q,
+                            const mgt_mx4* qt, void* stream);
+
+/* y [rows][cols] (dtype, row stride ldy) = what q stands for; exact in bf16 for MGT_MXFP4 and for
+ * MGT_NVFP4 with a power of two as factor (inside bf16's range). */
+mgt_status mgt_mx4_dequantize(const mgt_mx4* q, int32_t dtype, void* y, int64_t ldy, void* stream);
+
+/* C [A.rows][B.rows] = A B^T (c_dtype MGT_F32 or MGT_BF16, row stride ldc), sums in fp32 on the
+ * tensor cores with both operands' scales applied there, factors applied to the sum. Any number
+ * of rows from one up (few rows take a path that splits the sum over SMs); cols are the summed
+ * axis and equal. `status`: int32 device word, zeroed by the caller, that receives timeout codes
+ * as in mgt_gemm_fp8. */
+mgt_status mgt_gemm_mx4(const mgt_mx4* A, const mgt_mx4* B, void* C, int32_t c_dtype, int64_t ldc,
+                        int32_t* status, void* stream);
+
+/* Both projections of a gated feed-forward block with its activation and product:
+ *   [gate | up] = X W^T,   a = Q(act(gate) * up)
+ * W holds ffn = a->cols gate rows from row 0 and as many up rows from row P = ffn rounded up to
+ * 128, W->rows = 2 P (rows between are not read into any result). gate, up and the activation
+ * stay in fp32; a ([X->rows][ffn]) leaves quantised, ready for the product with W2. u (optional,
+ * bf16, row stride ldu >= 2 ffn) receives [gate | up] for the backward. act: mgt_act, GeLU exact
+ * or tanh. For MGT_NVFP4 a->factor is an input: a kept scale. */
+mgt_status mgt_gemm_mx4_gated(const mgt_mx4* X, const mgt_mx4* W, int32_t act, const mgt_mx4* a,
+                              void* u, int64_t ldu, int32_t* status, void* stream);
+
+/* Backward of the gated product, quantised for the products that follow: from da = dL/da (bf16,
+ * [rows][ffn]) and u = [gate | up] (bf16, as above), in fp32
+ *   dgate = da * up * act'(gate),   dup = da * act(gate),   a = act(gate) * up
+ * du  [rows][2 P]: dgate from column 0, dup from column P (zeros behind each): dX = du W1^T^T with
+ *     W1^T laid out alike;
+ * dut [2 P][rows]: dgate^T from row 0, dup^T from row P: the weight gradients of gate and up;
+ * at  [ffn][rows]: a^T, for dW2. Any of them may be NULL, not all. MGT_NVFP4: factors are inputs. */
+mgt_status mgt_mx4_gated_bwd(int32_t act, int32_t rows, int32_t ffn, const void* da, int64_t ldda,
+                             const void* u, int64_t ldu, const mgt_mx4* du, const mgt_mx4* dut,
+                             const mgt_mx4* at, void* stream);
+
 /* Failure-path probe (diagnostics and tests; no counterpart in the pages). Launches one thread
  * that waits on a device barrier nothing ever arrives on, through the same bounded wait that
  * every pipelined kernel of this library uses; after limit_ns (0 < limit_ns <= 1e9) it gives

@@ -15,8 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmgt.so")
 SOURCES = ["gemm_tc.cu", "attn.cu", "attn_tc.cu", "ln_misc.cu", "layer.cu", "ln_noalloc.cu",
-           "fp8.cu", "layer_tp.cu"]
-HEADERS = ["mgt_device.cuh", "mgt_internal.h"]
+           "fp8.cu", "layer_tp.cu", "mx4.cu", "gemm_mx4.cu", "mx4_api.cu"]
+HEADERS = ["mgt_device.cuh", "mgt_internal.h", "mx4_device.cuh", "mx4_internal.h"]
 
 
 def nvcc_path() -> str:

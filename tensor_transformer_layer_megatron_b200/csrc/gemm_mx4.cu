@@ -1,0 +1,412 @@
+// Products of microscaled 4-bit operands on the tensor cores of sm_100a (tcgen05.mma with block
+// scaling: kind::mxf4 for 32-element blocks with 2^e scales, kind::mxf4nvf4 for 16-element blocks
+// with e4m3 scales; fp32 accumulators).
+//
+// C[m, n] = f_a f_b sum_b s_a(m, b) s_b(n, b) sum_{k in b} a(m, k) b(n, k): the tensor core takes
+// the two 4-bit operands from shared memory and their scales from tensor memory and applies the
+// scales inside the sum.
+#include <cudaTypedefs.h>
+
+#include "mx4_device.cuh"
+#include "mx4_internal.h"
+
+namespace mgt {
+namespace {
+
+// 2-D tiled bulk load into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_2d(const CUtensorMap* m, uint64_t* bar, void* dst, int c0,
+                                            int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// A 512-byte scale tile (128 rows by 4 blocks) to four tensor-memory columns: lane r % 32 of
+// column r / 32 gets the four bytes of row r, in all four lane quarters. The source is 32 rows
+// of 16 bytes, unswizzled: core matrices of 8 rows, 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFF);
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t smem_addr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(scale_desc(smem_addr))
+               : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: both operands e2m1 (1), K-major. `id` selects
+// the pair of scale bytes in a 32-bit scale word (mxfp4: 0 for the even 64-element step, 2 for
+// the odd one; nvfp4 uses all four).
+template <int FMT>
+__device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t id) {
+  return (1u << 7) | (1u << 10) | (id << 4) | ((uint32_t)(N >> 3) << 17) |
+         (FMT == kMxfp4 ? 1u << 23 : 0u) | ((uint32_t)(M >> 7) << 27) | (id << 29);
+}
+template <int FMT>
+__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (FMT == kMxfp4)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+constexpr int kStageK = 256;          // elements of K per stage: 128 bytes of a row
+constexpr int kPRows = 128;           // weight rows of a CTA's tile (per matrix)
+constexpr int kPBytes = kPRows * 128;
+
+// ---------------------------------------------------------------------------- weights as rows
+// The weights' rows take the 128 lanes of the accumulator and up to 256 tokens its columns, so a
+// few tokens cost no wasted operand traffic: each CTA streams its 128 weight rows once. The
+// summed axis is split over a cluster of up to eight CTAs, whose fp32 partial tiles meet in
+// distributed shared memory, added in rank order. Gated: two accumulators, gate and up rows of
+// the same outputs.
+struct SkinnyArgs {
+  int M, N, kp;                 // tokens, weight rows (per matrix), K rounded up to 128
+  int bnq, stages, tmem_cols;
+  const uint8_t* p_scales;
+  const uint8_t* p2_scales;
+  long long p_ld;
+  const uint8_t* q_scales;
+  long long q_ld;
+  const float *p_factor, *q_factor;
+  void* C;
+  int c_f32;
+  long long ldc;
+  int act;
+  Mx4Out a;
+  const float* out_factor;
+  __nv_bfloat16* u;
+  long long ldu;
+  int* err;
+};
+
+__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+template <int FMT, bool GATED>
+__global__ void __launch_bounds__(192)
+    mx4_skinny_kernel(const __grid_constant__ CUtensorMap tmP,
+                      const __grid_constant__ CUtensorMap tmP2,
+                      const __grid_constant__ CUtensorMap tmQ, const SkinnyArgs g) {
+  constexpr int NM = GATED ? 2 : 1;
+  constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;  // scale tiles per stage and 128 rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int groups = g.bnq > 128 ? 2 : 1;  // 128-row groups of the tokens' scales
+  const int stage_bytes = NM * kPBytes + g.bnq * 128;
+  const int sf_bytes = (NM + groups) * kTps * 512;
+  uint8_t* sf = smem + g.stages * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf + g.stages * sf_bytes);
+  uint64_t* empty = full + g.stages;
+  uint64_t* tfull = empty + g.stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const uint32_t rank = cluster_ctarank();
+  const int p0 = (int)(blockIdx.x / csize) * kPRows;
+  const int q0 = blockIdx.y * g.bnq;
+  const int ki = (g.kp + kStageK - 1) / kStageK;
+  const int k_begin = (int)((long long)ki * rank / csize);
+  const int k_end = (int)((long long)ki * (rank + 1) / csize);
+  const int k_tiles = g.kp / Mx4Fmt<FMT>::kTileCols;
+  // groups of 128 tokens that have scales in the buffer
+  const int q_groups = min(groups, (g.M - q0 + 127) / 128);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmP);
+    if (GATED) tma_prefetch_desc(&tmP2);
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, g.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t acc_cols = (uint32_t)(g.bnq + 31) & ~31u;
+  grid_dependency_wait();  // the operands are the previous kernel's results
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kt = k_begin; kt < k_end; ++kt) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, g.err, kErrTimeoutProducer, abort_flag)) break;
+        const int n = min(kTps, k_tiles - kt * kTps);  // scale tiles of this stage
+        mbar_arrive_expect_tx(&full[stage],
+                              (uint32_t)(stage_bytes + (NM + q_groups) * n * 512));
+        uint8_t* d = smem + stage * stage_bytes;
+        uint8_t* s = sf + stage * sf_bytes;
+        tma_load_2d(&tmP, &full[stage], d, kt * 128, p0);
+        if (GATED) tma_load_2d(&tmP2, &full[stage], d + kPBytes, kt * 128, p0);
+        tma_load_2d(&tmQ, &full[stage], d + NM * kPBytes, kt * 128, q0);
+        const long long pt = (long long)(p0 / 128) * (g.p_ld / Mx4Fmt<FMT>::kTileCols) + kt * kTps;
+        bulk_load_1d(s, g.p_scales + pt * 512, n * 512, &full[stage]);
+        if (GATED) bulk_load_1d(s + kTps * 512, g.p2_scales + pt * 512, n * 512, &full[stage]);
+        for (int q = 0; q < q_groups; ++q) {
+          const long long qt =
+              (long long)(q0 / 128 + q) * (g.q_ld / Mx4Fmt<FMT>::kTileCols) + kt * kTps;
+          bulk_load_1d(s + (NM + q) * kTps * 512, g.q_scales + qt * 512, n * 512, &full[stage]);
+        }
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      for (int i = 1; i <= g.stages; ++i) {  // every copy has landed before the CTA may exit
+        int s = stage - i;
+        uint32_t ph = phase;
+        if (s < 0) {
+          s += g.stages;
+          ph ^= 1;
+        }
+        mbar_wait(&full[s], ph, g.err, kErrTimeoutDrain, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t sf_cols = (uint32_t)(NM + groups) * kTps * 4;
+      for (int kt = k_begin; kt < k_end; ++kt) {
+        if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) break;
+        tc_fence_after();
+        const int n = min(kTps, k_tiles - kt * kTps);
+        const int steps = min(4, (g.kp - kt * kStageK) / 64);
+        // Each stage has scale columns of its own: they are rewritten only after the producer
+        // has seen the products of the stage's last use complete.
+        const uint32_t sc = tmem + NM * acc_cols + stage * sf_cols;
+        const uint32_t ss = smem_u32(sf + stage * sf_bytes);
+        for (int t = 0; t < n; ++t) {
+#pragma unroll
+          for (int m = 0; m < NM; ++m)
+            tc_cp_scales(sc + (m * kTps + t) * 4, ss + (m * kTps + t) * 512);
+          for (int q = 0; q < groups; ++q)
+            tc_cp_scales(sc + (NM * kTps + t * groups + q) * 4, ss + ((NM + q) * kTps + t) * 512);
+        }
+        const uint32_t pa = smem_u32(smem + stage * stage_bytes);
+        const uint32_t qa = pa + NM * kPBytes;
+        for (int k = 0; k < steps; ++k) {
+          const int t = FMT == kMxfp4 ? k >> 1 : k;
+          const uint32_t id = FMT == kMxfp4 ? (uint32_t)(k & 1) * 2 : 0u;
+          const uint32_t idesc = idesc_mx4<FMT>(kPRows, g.bnq, id);
+          const uint64_t qd = smem_desc_sw128(qa + k * 32, 16, 1024);
+#pragma unroll
+          for (int m = 0; m < NM; ++m)
+            tc_mma_mx4<FMT>(tmem + m * acc_cols, smem_desc_sw128(pa + m * kPBytes + k * 32, 16, 1024),
+                            qd, idesc, sc + (m * kTps + t) * 4, sc + (NM * kTps + t * groups) * 4,
+                            (kt > k_begin || k > 0) ? 1u : 0u);
+        }
+        tc_commit(&empty[stage]);
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      tc_commit(tfull);
+      mbar_wait(tfull, 0, g.err, kErrTimeoutDrain, nullptr);
+    }
+    __syncwarp();
+  }
+
+  // Partial tiles [matrix][token][128] in the operand stages' memory: all copies into it have
+  // been consumed once the last product has completed.
+  float* part = reinterpret_cast<float*>(smem);
+  const bool epi = warp >= 2;
+  const int ew = warp & 3;
+  const int p = ew * 32 + lane;
+  bool ok = true;
+  if (epi) {
+    ok = mbar_wait(tfull, 0, g.err, kErrTimeoutEpilogue, abort_flag) && !*abort_flag;
+    tc_fence_after();
+    if (ok) {
+#pragma unroll 1
+      for (int m = 0; m < NM; ++m)
+#pragma unroll 1
+        for (int c = 0; c < (int)acc_cols; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + m * acc_cols + c + ((uint32_t)(ew * 32) << 16), v);
+          float* o = part + (m * g.bnq + c) * kPRows + p;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < g.bnq) o[i * kPRows] = v[i];
+        }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, g.tmem_cols);
+  }
+  if (epi && ok) {
+    const float f = (g.p_factor ? g.p_factor[1] : 1.f) * (g.q_factor ? g.q_factor[1] : 1.f);
+    const int tokens = min(g.bnq, g.M - q0);
+    const uint32_t mine = smem_u32(part + p);
+    const float inv_f = GATED && FMT == kNvfp4 ? 1.0f / (g.out_factor ? g.out_factor[1] : 1.f) : 1.f;
+#pragma unroll 1
+    for (int t = (int)rank; t < tokens; t += (int)csize) {
+      float v[NM];
+#pragma unroll
+      for (int m = 0; m < NM; ++m) v[m] = 0.f;
+      for (uint32_t r = 0; r < csize; ++r)
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          v[m] += ld_dsmem(mapa_shared(mine + (uint32_t)((m * g.bnq + t) * kPRows * 4), r));
+      const long long row = q0 + t;
+      const int col = p0 + p;
+      if constexpr (!GATED) {
+        if (col < g.N) {
+          if (g.c_f32)
+            static_cast<float*>(g.C)[row * g.ldc + col] = v[0] * f;
+          else
+            static_cast<__nv_bfloat16*>(g.C)[row * g.ldc + col] = __float2bfloat16_rn(v[0] * f);
+        }
+      } else {
+        const float gate = v[0] * f, up = v[NM - 1] * f;
+        if (g.u && col < g.N) {
+          g.u[row * g.ldu + col] = __float2bfloat16_rn(gate);
+          g.u[row * g.ldu + g.N + col] = __float2bfloat16_rn(up);
+        }
+        float h, dh;
+        gate_and_grad(gate, g.act, h, dh);
+        const float a = col < g.N ? h * up : 0.f;  // columns behind the last are zeros
+        constexpr int B = Mx4Fmt<FMT>::kBlock;
+        uint32_t mx = abs_bits(a);
+#pragma unroll
+        for (int o = B / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const Mx4Block q = mx4_block<FMT>(mx, inv_f);
+        const float x = mx4_scaled<FMT>(a, q, inv_f);
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __shfl_down_sync(0xffffffffu, x, i);
+        if (lane % 8 == 0)
+          *reinterpret_cast<uint32_t*>(g.a.codes + (row * g.a.ld + col) / 2) = e2m1x8(w) & q.mask;
+        if (lane % B == 0)
+          g.a.scales[mx4_scale_off<FMT>(row, col / B, g.a.ld)] = (uint8_t)q.byte;
+      }
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
+}
+
+// ---------------------------------------------------------------------------- host side
+bool map_codes(CUtensorMap* m, const uint8_t* codes, int rows, int kp, long long ld, int box_rows) {
+  return make_tensor_map_u8_2d(m, codes, (uint64_t)kp / 2, (uint64_t)rows, (uint64_t)ld / 2,
+                               (uint32_t)box_rows);
+}
+
+template <int FMT, bool GATED>
+cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
+  constexpr int NM = GATED ? 2 : 1;
+  constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;
+  const int most = GATED ? 128 : 256;
+  int bnq = 16;
+  while (bnq < g.M && bnq < most) bnq *= 2;
+  const int groups = bnq > 128 ? 2 : 1;
+  const int kp = (g.K + 127) & ~127, ki = (kp + kStageK - 1) / kStageK;
+  const int tiles = ((g.N + kPRows - 1) / kPRows) * ((g.M + bnq - 1) / bnq);
+  int split = 1;
+  while (split < 8 && split * 2 <= ki && tiles * split * 2 <= 2 * num_sms) split *= 2;
+
+  const int stage_bytes = NM * kPBytes + bnq * 128 + (NM + groups) * kTps * 512;
+  const int acc = NM * ((bnq + 31) & ~31);
+  const int sf_cols = (NM + groups) * kTps * 4;
+  const int room = 227 * 1024 - 2048;
+  const int half = 113 * 1024 - 2048;
+  int stages = half / stage_bytes;  // two CTAs per SM where three stages fit
+  if (stages < 3 || acc + 3 * sf_cols > 256) {
+    stages = room / stage_bytes;
+    while (acc + stages * sf_cols > 512) --stages;
+  } else {
+    while (acc + stages * sf_cols > 256) --stages;
+  }
+  int cols = 32;
+  while (cols < acc + stages * sf_cols) cols *= 2;
+  const size_t smem = 1024 + (size_t)stages * stage_bytes + 16 * stages + 64;
+
+  const int up0 = (g.N + 127) & ~127;  // first up row of a gated weight operand
+  CUtensorMap tp, tp2, tq;
+  if (!map_codes(&tp, g.B.codes, g.N, kp, g.B.ld, kPRows) ||
+      !map_codes(&tp2, g.B.codes + (GATED ? up0 * g.B.ld / 2 : 0), g.N, kp, g.B.ld, kPRows) ||
+      !map_codes(&tq, g.A.codes, g.M, kp, g.A.ld, bnq))
+    return cudaErrorInvalidValue;
+  SkinnyArgs a = {};
+  a.M = g.M; a.N = g.N; a.kp = kp;
+  a.bnq = bnq; a.stages = stages; a.tmem_cols = cols;
+  a.p_scales = g.B.scales;
+  a.p2_scales = g.B.scales + (up0 / 128) * (g.B.ld / Mx4Fmt<FMT>::kTileCols) * 512;
+  a.p_ld = g.B.ld;
+  a.q_scales = g.A.scales; a.q_ld = g.A.ld;
+  a.p_factor = g.b_factor; a.q_factor = g.a_factor;
+  a.C = g.C; a.c_f32 = g.c_f32; a.ldc = g.ldc;
+  a.act = g.act; a.a = g.a; a.out_factor = g.out_factor;
+  a.u = static_cast<__nv_bfloat16*>(g.u); a.ldu = g.ldu;
+  a.err = g.err;
+
+  auto kern = mx4_skinny_kernel<FMT, GATED>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       227 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((g.N + kPRows - 1) / kPRows) * split),
+                     (unsigned)((g.M + bnq - 1) / bnq));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tp, tp2, tq, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mx4(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
+  if (g.fmt == kMxfp4)
+    return g.gated ? launch_skinny<kMxfp4, true>(g, num_sms, s)
+                   : launch_skinny<kMxfp4, false>(g, num_sms, s);
+  return g.gated ? launch_skinny<kNvfp4, true>(g, num_sms, s)
+                 : launch_skinny<kNvfp4, false>(g, num_sms, s);
+}
+
+}  // namespace mgt

@@ -1,0 +1,147 @@
+// Microscaled 4-bit floating point: the block formats, shared by the quantisers (mx4.cu) and the
+// products' fused epilogues (gemm_mx4.cu).
+//
+// An element is e2m1 (1 sign, 2 exponent, 1 mantissa bit): +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}. Blocks
+// run along the summed axis. MXFP4 (OCP Microscaling Formats v1.0): 32 elements share 2^e, held
+// as the byte e + 127, e = floor(log2 amax) - 2. NVFP4: 16 elements share an e4m3 scale
+// s = e4m3(amax / (6 f)), and the tensor a factor f.
+//
+// Every rounding decision is the one exact arithmetic takes: x 2^-e is exact in fp32, and so is
+// x / f for a power of two f; x / (f s) is a correctly rounded quotient, which can meet a border
+// between two elements (at most 3 significant bits) only where the exact quotient does: x / f
+// and border * s (at most 7 bits) differ by at least one unit in the 24th bit of x / f, more
+// than half a unit of the quotient.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "mgt_device.cuh"
+
+namespace mgt {
+
+constexpr int kMxfp4 = 0;
+constexpr int kNvfp4 = 1;
+
+template <int FMT>
+struct Mx4Fmt {
+  static constexpr int kBlock = FMT == kMxfp4 ? 32 : 16;  // elements that share a scale
+  static constexpr int kTileCols = 4 * kBlock;            // columns of one 512-byte scale tile
+};
+
+// Byte offset of the scale of row r, block b in an operand of leading dimension ld: tiles of
+// 128 rows by 4 blocks, in a tile 16 (r % 32) + 4 (r % 128 / 32) + b % 4. That is the order in
+// which tcgen05.cp (32x128b, four warps) fills four tensor-memory columns.
+template <int FMT>
+__device__ __forceinline__ long long mx4_scale_off(long long r, int b, long long ld) {
+  return ((r >> 7) * (ld / Mx4Fmt<FMT>::kTileCols) + (b >> 2)) * 512 + 16 * (r & 31) +
+         4 * ((r >> 5) & 3) + (b & 3);
+}
+
+// What a block's elements are multiplied by, and the byte that stands for its scale.
+struct Mx4Block {
+  float inv;      // mxfp4: 2^-e. nvfp4: 1 / s, correctly rounded (0 for a block of zeros)
+  float s;        // nvfp4: s
+  uint32_t byte;  // mxfp4: e + 127 (255 = NaN). nvfp4: e4m3 (0x7f = NaN)
+  uint32_t mask;  // codes are ANDed with it: 0 for a block without a usable scale
+};
+
+// From the largest |x| of the block as fp32 bits (NaN above infinity above every number). A
+// block that holds an infinity or a NaN gets the scale NaN and zero codes.
+template <int FMT>
+__device__ __forceinline__ Mx4Block mx4_block(uint32_t amax_bits, float inv_f) {
+  Mx4Block q;
+  if constexpr (FMT == kMxfp4) {
+    const int eb = (int)(amax_bits >> 23);  // floor(log2 amax) + 127; 0 for subnormals
+    q.byte = eb == 255 ? 255u : (uint32_t)max(eb - 2, 0);
+    q.inv = __uint_as_float((254u - q.byte) << 23);
+    q.s = 0.f;
+    q.mask = eb == 255 ? 0u : 0xffffffffu;
+    if (eb == 255) q.inv = 0.f;
+  } else {
+    const float t = fminf(__uint_as_float(amax_bits) * inv_f, 3.4028234e38f) / 6.0f;
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(t));
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(e));
+    q.s = __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+    const bool bad = amax_bits >= 0x7f800000u;
+    q.byte = bad ? 0x7fu : (uint32_t)(e & 0xffu);
+    q.mask = (bad || q.s == 0.f) ? 0u : 0xffffffffu;
+    q.inv = q.mask ? __frcp_rn(q.s) : 0.f;
+  }
+  return q;
+}
+
+// The scaled element. nvfp4: (x / f) / s by a product with the rounded reciprocal and one
+// residual correction, which gives the correctly rounded quotient (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000 processor, 1990: theorem 1).
+template <int FMT>
+__device__ __forceinline__ float mx4_scaled(float x, const Mx4Block& q, float inv_f) {
+  if constexpr (FMT == kMxfp4) {
+    return x * q.inv;
+  } else {
+    const float xs = fmaxf(fminf(x * inv_f, 3.4028234e38f), -3.4028234e38f);
+    const float y = xs * q.inv;
+    return fmaf(fmaf(-y, q.s, xs), q.inv, y);
+  }
+}
+
+// Eight fp32 values to eight e2m1 codes (round to nearest, ties to even, saturating at 6), the
+// first in the low four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{ .reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3}; }"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], const Mx4Block& q,
+                                               float inv_f) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mx4_scaled<FMT>(x[i], q, inv_f);
+  return e2m1x8(v) & q.mask;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The fp32 value of a scale byte (without the tensor's factor).
+template <int FMT>
+__device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
+  if constexpr (FMT == kMxfp4) {
+    if (byte == 255u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(byte ? byte << 23 : 0x00400000u);  // 2^-127 is subnormal
+  } else {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)byte));
+    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+  }
+}
+
+// Activation of a gated block and its derivative. act: 0 silu, 1 gelu (erf), 2 gelu (tanh). A
+// block's scale follows its largest value, so a value counts by its relative error however small
+// it is: Phi(z) = erfc(-z / sqrt 2) / 2 and (1 + tanh y) / 2 = 1 / (1 + e^-2y) keep it in the
+// negative tail, where 1 + erf and 1 + tanh cancel.
+__device__ __forceinline__ void gate_and_grad(float z, int act, float& h, float& dh) {
+  if (act == 0) {
+    silu_and_grad_f(z, h, dh);
+  } else if (act == 1) {
+    const float c = 0.5f * erfcf(z * -0.7071067811865476f);
+    h = z * c;
+    dh = fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), c);
+  } else {
+    const float k = 0.7978845608028654f;  // sqrt(2 / pi)
+    const float z2 = z * z;
+    const float s = 1.0f / (1.0f + expf(-2.0f * k * z * fmaf(0.044715f, z2, 1.0f)));
+    h = z * s;
+    dh = s * fmaf(z * (1.0f - s), 2.0f * k * fmaf(0.134145f, z2, 1.0f), 1.0f);
+  }
+}
+
+}  // namespace mgt

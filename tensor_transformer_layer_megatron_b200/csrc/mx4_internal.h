@@ -1,0 +1,50 @@
+// Declarations shared by the microscaled 4-bit kernels and their C ABI.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mgt {
+
+// A 4-bit operand: packed codes (rows of ld / 2 bytes), scale tiles, leading dimension.
+struct Mx4Out {
+  uint8_t* codes;
+  uint8_t* scales;
+  long long ld;
+};
+
+// C[m, n] = f_a f_b sum_k A(m, k) B(n, k): A [M][K] activations, B [N][K] weights. Gated: B holds
+// gate rows 0 .. N-1 and up rows from N rounded up to 128; the result act(gate) * up leaves
+// quantised in `a` (and gate, up in bf16 in u, where given) instead of in C.
+struct Mx4Gemm {
+  int fmt, M, N, K;
+  Mx4Out A, B;
+  const float* a_factor;  // {amax, factor} of the tensor; null: 1
+  const float* b_factor;
+  void* C;
+  int c_f32;
+  long long ldc;
+  int gated, act;
+  Mx4Out a;
+  const float* out_factor;
+  void* u;
+  long long ldu;
+  int* err;
+};
+cudaError_t launch_gemm_mx4(const Mx4Gemm& g, int num_sms, cudaStream_t s);
+
+// fmt: 0 mxfp4, 1 nvfp4; dtype: 0 fp32, 1 bf16. factor (nvfp4): {amax, f}.
+cudaError_t launch_mx4_factor(int dtype, int rows, int cols, const void* x, long long ldx,
+                              float* out, int num_sms, cudaStream_t s);
+cudaError_t launch_mx4_quantize(int fmt, int dtype, int rows, int cols, const void* x,
+                                long long ldx, const float* factor, const Mx4Out& out,
+                                const Mx4Out& out_t, int num_sms, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(int fmt, int dtype, int rows, int cols, const Mx4Out& q,
+                                  const float* factor, void* y, long long ldy, int num_sms,
+                                  cudaStream_t s);
+cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* da,
+                                 long long ldda, const void* u, long long ldu, const float* f_du,
+                                 const float* f_dut, const float* f_at, const Mx4Out& dg,
+                                 const Mx4Out& dup, const Mx4Out& dgt, const Mx4Out& dupt,
+                                 const Mx4Out& at, cudaStream_t s);
+
+}  // namespace mgt

@@ -1,0 +1,427 @@
+"""4-bit operators on the GPU against the float64 oracle: quantisation byte by byte, products and
+the gated block over ragged sizes, parts of wider operands, rows and columns that must stay as
+they were, streams, and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import tensor_transformer_layer_megatron_b200 as mgt
+from oracle import mx4
+
+pytestmark = pytest.mark.gpu
+FMTS = ["mxfp4", "nvfp4"]
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def randn(*n, seed=0, scale=1.0, dtype=torch.float32):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return (torch.randn(*n, generator=g) * scale).to(dtype)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def unsigned_zero(packed):
+    """Packed codes with -0 as 0 (the sign of a zero is not specified)."""
+    lo, hi = packed & 15, packed >> 4
+    return np.where(lo == 8, 0, lo) | (np.where(hi == 8, 0, hi) << 4)
+
+
+def operand(fmt, rows, cols, x=None, f=1.0, fill=0xCB):
+    """An operand whose buffers hold a pattern before it is written."""
+    q = mgt.Mx4(fmt, rows, cols)
+    q.codes.fill_(fill)
+    q.scales.fill_(fill)
+    if fmt == "nvfp4":
+        q.factor.copy_(torch.tensor([0.0, f]))
+    if x is not None:
+        mgt.mx4_quantize(x, q)
+    return q
+
+
+def check_bytes(q, x, f, fill=0xCB):
+    codes, byte, _ = mx4.quantize(x, q.fmt, f)
+    packed, tiles = mx4.pack(codes, byte)
+    assert np.array_equal(unsigned_zero(q.codes.cpu().numpy()), unsigned_zero(packed))
+    got = q.scales.cpu().numpy().astype(np.int16)
+    assert np.array_equal(got, np.where(tiles < 0, fill, tiles))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 31, 0), (2, 33, 7), (3, 128, 8), (5, 129, 0),
+                                           (64, 256, 0), (65, 300, 4), (130, 515, 1), (257, 1000, 24)])
+def test_quantize_both_layouts(fmt, dtype, rows, cols, pad):
+    x = randn(rows, cols + pad, seed=rows + cols, scale=3.0, dtype=TYPES[dtype])
+    x[:, : cols // 2] *= 2.0 ** -7
+    x[rows // 2, :] = 0  # a block of zeros in every row-wise group of that row
+    xd = x.cuda()[:, :cols]
+    f, fac = 1.0, None
+    if fmt == "nvfp4":
+        fac = torch.full((2,), -3.0, device="cuda")
+        mgt.mx4_tensor_factor(xd, fac)
+        amax, f = mx4.tensor_factor(np64(xd))
+        assert fac.tolist() == [np.float32(amax), f]
+    for t in (False, True):
+        q, qt = operand(fmt, rows, cols), operand(fmt, cols, rows)
+        if fac is not None:
+            q.factor.copy_(fac)
+            qt = mgt.Mx4(fmt, cols, rows, codes=qt.codes, scales=qt.scales, factor=q.factor)
+        mgt.mx4_quantize(xd, q, qt if t else None)
+        check_bytes(q, np64(xd), f)
+        if t:
+            check_bytes(qt, np64(xd).T, f)
+    mgt.mx4_quantize(xd, None, qt)
+    check_bytes(qt, np64(xd).T, f)
+    for name, dt in TYPES.items():  # and back, exactly, into rows of a wider matrix
+        y = torch.full((rows, cols + 3), 7.0, dtype=dt, device="cuda")
+        mgt.mx4_dequantize(q, y[:, :cols])
+        assert np.array_equal(np64(y[:, :cols]), mx4.values(np64(xd), fmt, f))
+        assert (y[:, cols:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_every_tie_and_its_neighbours(fmt):
+    """Borders between elements, and the fp32 numbers next to them, for every scale of a block."""
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    n = mx4.BLOCK[fmt]
+    rows = []
+    scales = [2.0 ** e for e in (-126, -30, 0, 90)] if fmt == "mxfp4" else \
+        [(8 + m) / 8 * 2.0 ** e for m in range(8) for e in (-6, 0, 7)] + [2.0 ** -9, 3 * 2.0 ** -9]
+    for s in scales:
+        b = (borders * np.float32(s)).astype(np.float32)
+        v = np.stack([b, np.nextafter(b, np.float32(0)), np.nextafter(b, np.float32(3e38))]).reshape(-1)
+        for lot in (v[:15], v[-15:]):
+            r = np.zeros(n, np.float32)
+            r[0] = 6 * s if fmt == "nvfp4" else 4 * s  # gives the block the scale s
+            r[1:16] = lot if fmt == "nvfp4" else np.minimum(lot, np.float32(7.9 * s))
+            rows.append(r * np.where(np.arange(n) % 2, -1, 1).astype(np.float32))
+    x = torch.tensor(np.array(rows))
+    for y in (x, x.t().contiguous()):
+        q, qt = operand(fmt, *y.shape), operand(fmt, y.shape[1], y.shape[0])
+        if fmt == "nvfp4":
+            qt = mgt.Mx4(fmt, qt.rows, qt.cols, codes=qt.codes, scales=qt.scales, factor=q.factor)
+        mgt.mx4_quantize(y.cuda(), q, qt)
+        check_bytes(q, np64(y), 1.0)
+        check_bytes(qt, np64(y).T, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_non_finite_subnormal_and_huge(fmt, dtype):
+    x = randn(40, 200, seed=9, dtype=TYPES[dtype])
+    x[0, 5], x[1, 70], x[2, 199], x[39, 0] = float("inf"), float("nan"), -float("inf"), float("nan")
+    x[3] *= 2.0 ** -126
+    x[4] *= 2.0 ** -133  # subnormal
+    x[5] *= 2.0 ** 100
+    x[6, :] = torch.finfo(TYPES[dtype]).max
+    xd = x.cuda()
+    q, qt = operand(fmt, 40, 200), operand(fmt, 200, 40)
+    f = 1.0
+    if fmt == "nvfp4":
+        qt = mgt.Mx4(fmt, 200, 40, codes=qt.codes, scales=qt.scales, factor=q.factor)
+        mgt.mx4_tensor_factor(xd, q.factor)
+        amax, f = mx4.tensor_factor(np64(xd))
+        assert q.factor.tolist() == [amax, f]
+    for g in ([f] if fmt == "mxfp4" else [f, 2.0 ** -100]):  # also a factor far too small: saturation
+        if fmt == "nvfp4":
+            q.factor[1] = g
+        mgt.mx4_quantize(xd, q, qt)
+        check_bytes(q, np64(xd), g)
+        check_bytes(qt, np64(xd).T, g)
+        y = torch.empty(40, 200, device="cuda")
+        mgt.mx4_dequantize(q, y)
+        assert np.array_equal(np64(y), mx4.values(np64(xd), fmt, g).astype(np.float32), equal_nan=True)
+
+
+def product_bound(a, b, bf16, ref):
+    """Per element. Products of two elements and two scales have few bits and are exact; the tensor
+    core adds 64 of them to the fp32 accumulator at a time, each time within 4 units in the last
+    place of the largest partial sum (alignment of the addends and one rounding; a unit is at most
+    2^-23 of it), and the partial sums stay below sum |a b|. The result then meets the factor (two
+    fp32 products, 2^-24 each) and the rounding to bf16 (2^-8)."""
+    steps = -(-a.shape[1] // 64)
+    t = np.abs(a) @ np.abs(b).T * (4 * steps * 2.0 ** -23) + np.abs(ref) * 2.0 ** -23
+    return t + (np.abs(ref) * 2.0 ** -8 if bf16 else 0) + 1e-37
+
+
+SHAPES = [(1, 1, 1), (1, 8, 16), (2, 130, 33), (1, 4096, 1024), (7, 257, 4096), (16, 128, 128),
+          (17, 100, 300), (64, 513, 640), (100, 384, 2000), (128, 128, 256), (129, 129, 144),
+          (250, 1000, 777), (300, 520, 4096), (512, 256, 512), (777, 1111, 999), (1500, 640, 384)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(M, N, K, fmt, out):
+    x, w = randn(M, K, seed=M + N, scale=2.0), randn(N, K, seed=K, scale=0.05)
+    fx, fw = (1.0, 1.0) if fmt == "mxfp4" else (2.0 ** -6, 2.0 ** -11)
+    A, B = operand(fmt, M, K, x.cuda(), fx, 0xFF), operand(fmt, N, K, w.cuda(), fw, 0xFF)
+    a, b = mx4.values(np64(x), fmt, fx), mx4.values(np64(w), fmt, fw)
+    ref = a @ b.T
+    for pad in (0, 3, 8):
+        C = torch.full((M + 1, N + pad), 77.0, dtype=TYPES[out], device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        mgt.gemm_mx4(A, B, C[:M, :N], st)
+        assert int(st) == 0
+        err = np.abs(np64(C[:M, :N]) - ref)
+        bound = product_bound(a, b, out == "bf16", ref)
+        assert (err <= bound).all(), (err / bound).max()
+        assert (C[M] == 77).all() and (C[:, N:] == 77).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_product_carries_infinities_and_nans(fmt):
+    """A block that cannot be scaled makes the sums that it enters NaN, and no others."""
+    x, w = randn(40, 300, seed=1), randn(200, 300, seed=2)
+    x[3, 7], w[150, 299] = float("inf"), float("nan")
+    A, B = operand(fmt, 40, 300, x.cuda()), operand(fmt, 200, 300, w.cuda())
+    C = torch.zeros(40, 200, device="cuda")
+    mgt.gemm_mx4(A, B, C, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    want = np.zeros((40, 200), bool)
+    want[3], want[:, 150] = True, True
+    assert np.array_equal(np.isnan(np64(C)), want) and np.isfinite(np64(C))[~want].all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_parts_of_wider_operands(fmt):
+    """A product over columns 128 .. 427 and rows 256 .. of one operand, quantised there in place."""
+    q, w = operand(fmt, 400, 640, fill=0xFF), operand(fmt, 500, 300)
+    x, y = randn(144, 300, seed=4), randn(500, 300, seed=5)
+    part = q.part(256, 144, 128, 300)
+    mgt.mx4_quantize(x.cuda(), part)
+    mgt.mx4_quantize(y.cuda(), w)
+    untouched = q.codes.clone()
+    untouched[256:400, 64:64 + 192] = 255
+    assert (untouched == 255).all()
+    C, st = torch.empty(144, 500, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mgt.gemm_mx4(part, w, C, st)
+    a, b = mx4.values(np64(x), fmt), mx4.values(np64(y), fmt)
+    assert (np.abs(np64(C) - a @ b.T) <= product_bound(a, b, False, a @ b.T)).all()
+    D = torch.empty(500, 144, device="cuda")
+    mgt.gemm_mx4(w, part, D, st)
+    assert (np.abs(np64(D) - b @ a.T) <= product_bound(b, a, False, b @ a.T)).all()
+    back = torch.empty(144, 300, device="cuda")
+    mgt.mx4_dequantize(part, back)
+    assert np.array_equal(np64(back), a)
+
+
+def check_near(q, exact, f, eps, most=0.02):
+    """q holds exact (float64), each entry computed within eps of its size (and of its block's) before the
+    rounding to 4 bits: where exact (1 - eps) and exact (1 + eps) round alike, q must agree."""
+    y = torch.empty(q.rows, q.cols, device="cuda")
+    mgt.mx4_dequantize(q, y)
+    got = np64(y)
+    lo, hi = mx4.values(exact * (1 - eps), q.fmt, f), mx4.values(exact * (1 + eps), q.fmt, f)
+    sure = lo == hi
+    assert sure.mean() > 1 - most, sure.mean()
+    assert np.array_equal(got[sure], lo[sure]), np.abs(got - lo)[sure].max()
+    # the others: no further than the scale's rounding (2^-4) and one step (half of the value, or s / 2)
+    s = np.abs(exact).max() + 1e-30
+    assert (np.abs(got - exact)[~sure] <= 0.6 * np.abs(exact)[~sure] + 0.3 * s).all()
+
+
+def gated_weights(fmt, F, K, f, seed):
+    """Gate and up rows in one operand, rows and scales between them NaN where the format has one."""
+    P = (F + 127) // 128 * 128
+    w = randn(2 * F, K, seed=seed, scale=0.06)
+    q = operand(fmt, 2 * P, K, f=f, fill=0xFF)
+    mgt.mx4_quantize(w[:F].cuda(), q.rows_view(0, F))
+    mgt.mx4_quantize(w[F:].cuda(), q.rows_view(P, F))
+    return q, mx4.values(np64(w[:F]), fmt, f), mx4.values(np64(w[F:]), fmt, f)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,F,K", [(1, 1, 16), (1, 300, 512), (5, 128, 100), (33, 257, 640), (128, 64, 256),
+                                   (200, 500, 333), (300, 1300, 512), (700, 384, 128)])
+def test_gated_product(M, F, K, fmt, act):
+    x = randn(M, K, seed=M)
+    fx, fw, fa = (1.0,) * 3 if fmt == "mxfp4" else (2.0 ** -8, 2.0 ** -10, 2.0 ** -9)
+    X = operand(fmt, M, K, x.cuda(), fx, 0xFF)
+    W, wg, wu = gated_weights(fmt, F, K, fw, seed=F)
+    a = mx4.values(np64(x), fmt, fx)
+    g, u = a @ wg.T, a @ wu.T
+    h = mx4.act(g, act)[0] * u
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = []
+    for keep in (True, False):
+        q = operand(fmt, M, F, f=fa)
+        ub = torch.full((M, 2 * F + 5), 3.0, dtype=torch.bfloat16, device="cuda") if keep else None
+        mgt.gemm_mx4_gated(X, W, q, st, act=act, u=ub[:, :2 * F] if keep else None)
+        assert int(st) == 0
+        # columns behind the last are zeros, of scale zero
+        P = (F + 127) // 128 * 128
+        y = torch.empty(M, P, device="cuda")
+        mgt.mx4_dequantize(mgt.Mx4(fmt, M, P, codes=q.codes, scales=q.scales, factor=q.factor), y)
+        assert (y[:, F:] == 0).all()
+        # gate and up are within the product's bound; act and the product add a few 2^-23, and the
+        # activation's slope relative to its value is below 1 + |g|: 64 * 2^-23 covers |g| < 16 and
+        # sums that cancel to a quarter of their terms' root mean square
+        check_near(q, h, fa, 2.0 ** -15)
+        outs.append((q.codes.clone(), q.scales.clone()))
+        if keep:
+            ref = np.concatenate([g, u], 1)
+            bound = product_bound(a, np.concatenate([wg, wu]), True, ref)
+            assert (np.abs(np64(ub[:, :2 * F]) - ref) <= bound).all()
+            assert (ub[:, 2 * F:] == 3).all()
+    assert all(torch.equal(v, w) for v, w in zip(*outs))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,F", [(1, 1), (3, 200), (64, 128), (130, 515), (257, 300)])
+def test_gated_backward(M, F, fmt, act):
+    da = randn(M, F + 3, seed=M, scale=1e-3, dtype=torch.bfloat16)
+    u = randn(M, 2 * F + 1, seed=F, scale=2.0, dtype=torch.bfloat16)
+    P = (F + 127) // 128 * 128
+    fd, fa = (1.0, 1.0) if fmt == "mxfp4" else (2.0 ** -18, 2.0 ** -8)
+    dad, ud = da.cuda()[:, :F], u.cuda()[:, :2 * F]
+    dg, dup, a = mx4.gated_bwd(np64(dad), np64(ud[:, :F]), np64(ud[:, F:]), act)
+    full = [operand(fmt, M, 2 * P, f=fd), operand(fmt, 2 * P, M, f=fd), operand(fmt, F, M, f=fa)]
+    mgt.mx4_gated_bwd(dad, ud, *full, act=act)
+    du, dut, at = full
+    # two or three fp32 products and an activation within a few units of 2^-23; where act' crosses zero
+    # it is the difference of terms of size 1
+    eps = 2.0 ** -17
+    check_near(du.part(0, M, 0, F), dg, fd, eps)
+    check_near(du.part(0, M, P, F), dup, fd, eps)
+    check_near(dut.rows_view(0, F), dg.T, fd, eps)
+    check_near(dut.rows_view(P, F), dup.T, fd, eps)
+    check_near(at, a.T, fa, eps)
+    pad = torch.empty(M, 2 * P, device="cuda")
+    mgt.mx4_dequantize(du, pad)
+    assert (pad[:, F:P] == 0).all() and (pad[:, P + F:] == 0).all()
+    for k in range(3):  # one output at a time gives the same bytes
+        q = operand(fmt, full[k].rows, full[k].cols, f=(fd, fd, fa)[k])
+        mgt.mx4_gated_bwd(dad, ud, *[q if i == k else None for i in range(3)], act=act)
+        assert torch.equal(q.codes, full[k].codes) and torch.equal(q.scales, full[k].scales)
+
+
+def rel(got, ref):
+    return float(np.linalg.norm(np64(got) - ref) / np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,H,F", [(1, 256, 384), (96, 256, 700), (300, 512, 1000)])
+def test_gated_block_forward_and_backward(M, H, F, fmt):
+    """A training step through the block, every tensor in 4 bits where a product reads it. bf16
+    results are within 2^-9 root mean square of the exact ones (at most 2^-8 each), and the 4-bit
+    decisions of `a` and of the gradients that fp32 takes otherwise than float64 (fewer than one in
+    10^4, each off by at most half of its value) add less than 2^-8 to that."""
+    P = (F + 127) // 128 * 128
+    x, dy = randn(M, H, seed=1).bfloat16().cuda(), randn(M, H, seed=2, scale=1e-2).bfloat16().cuda()
+    w1, w2 = randn(2 * F, H, seed=3, scale=0.06).cuda(), randn(H, F, seed=4, scale=0.05).cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fx, fw, fa, fd = (1.0,) * 4 if fmt == "mxfp4" else (2.0 ** -8, 2.0 ** -11, 2.0 ** -8, 2.0 ** -14)
+
+    def op(r, c, f):
+        return operand(fmt, r, c, f=f, fill=0xFF)
+
+    def pair(r, c, f):
+        a, b = op(r, c, f), op(c, r, f)
+        return a, mgt.Mx4(fmt, c, r, codes=b.codes, scales=b.scales, factor=a.factor)
+
+    xq, xt = pair(M, H, fx)
+    mgt.mx4_quantize(x, xq, xt)
+    w1q, w1t = op(2 * P, H, fw), op(H, 2 * P, fw)
+    for k in (0, 1):
+        rows, cols = w1q.rows_view(k * P, F), w1t.part(0, H, k * P, F)
+        if fmt == "nvfp4":
+            cols.factor = rows.factor
+            cols._c.factor = rows._c.factor
+        mgt.mx4_quantize(w1[k * F:(k + 1) * F], rows, cols)
+    w2q, w2t = pair(H, F, fw)
+    mgt.mx4_quantize(w2, w2q, w2t)
+    a, u = op(M, F, fa), torch.empty(M, 2 * F, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    mgt.gemm_mx4_gated(xq, w1q, a, st, u=u)
+    mgt.gemm_mx4(a, w2q, y, st)
+    dyq, dyt = pair(M, H, fd)
+    mgt.mx4_quantize(dy, dyq, dyt)
+    da = torch.empty(M, F, dtype=torch.bfloat16, device="cuda")
+    mgt.gemm_mx4(dyq, w2t, da, st)
+    du, dut, at = op(M, 2 * P, fd), op(2 * P, M, fd), op(F, M, fa)
+    mgt.mx4_gated_bwd(da, u, du, dut, at)
+    dx = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    dwg, dwu = (torch.empty(F, H, device="cuda") for _ in range(2))
+    dw2 = torch.empty(H, F, device="cuda")
+    mgt.gemm_mx4(du, w1t, dx, st)
+    mgt.gemm_mx4(dut.rows_view(0, F), xt, dwg, st)
+    mgt.gemm_mx4(dut.rows_view(P, F), xt, dwu, st)
+    mgt.gemm_mx4(dyt, at, dw2, st)
+    assert int(st) == 0
+
+    v = lambda t, f: mx4.values(t if isinstance(t, np.ndarray) else np64(t), fmt, f)  # noqa: E731
+    xv, wg, wu = v(x, fx), v(w1[:F], fw), v(w1[F:], fw)
+    av = v(mx4.act(xv @ wg.T, "silu")[0] * (xv @ wu.T), fa)
+    assert rel(y, av @ v(w2, fw).T) < 2.0 ** -8
+    ug, uu = np64(u[:, :F]), np64(u[:, F:])  # what the backward reads is what the forward kept
+    assert rel(u, np.concatenate([xv @ wg.T, xv @ wu.T], 1)) < 2.0 ** -8
+    dav = v(dy, fd) @ v(np64(w2).T, fw).T
+    assert rel(da, dav) < 2.0 ** -8
+    dg, dup, ar = mx4.gated_bwd(np64(da), ug, uu, "silu")
+    xtv = v(np64(x).T, fx)
+    ref = v(dg, fd) @ v(np64(w1[:F]).T, fw).T + v(dup, fd) @ v(np64(w1[F:]).T, fw).T
+    assert rel(dx, ref) < 2.0 ** -8
+    assert rel(dwg, v(dg.T, fd) @ xtv.T) < 2.0 ** -8
+    assert rel(dwu, v(dup.T, fd) @ xtv.T) < 2.0 ** -8
+    assert rel(dw2, v(np64(dy).T, fd) @ v(ar.T, fa).T) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_streams_and_graphs_give_the_same_bytes(fmt):
+    """Eager on the current stream, on another one, on two at once, and replayed from a graph over
+    new inputs: the same bytes each time."""
+    M, F, K = 70, 600, 1024
+    x = [randn(M, K, seed=s).bfloat16().cuda() for s in (1, 2)]
+    W, _, _ = gated_weights(fmt, F, K, 2.0 ** -10 if fmt == "nvfp4" else 1.0, seed=3)
+    w2 = operand(fmt, K, F, randn(K, F, seed=4, scale=0.05).cuda(), 2.0 ** -10)
+
+    class Run:
+        def __init__(self):
+            self.x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+            self.q, self.a = operand(fmt, M, K), operand(fmt, M, F, f=2.0 ** -8)
+            self.y = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+            self.st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def go(self, stream=None):
+            if fmt == "nvfp4":
+                mgt.mx4_tensor_factor(self.x, self.q.factor, stream)
+            mgt.mx4_quantize(self.x, self.q, stream=stream)
+            mgt.gemm_mx4_gated(self.q, W, self.a, self.st, stream=stream)
+            mgt.gemm_mx4(self.a, w2, self.y, self.st, stream=stream)
+
+    want = []
+    for xi in x:
+        r = Run()
+        r.x.copy_(xi)
+        r.go()
+        want.append(r.y.clone())
+    runs, streams = [Run(), Run()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for r, xi in zip(runs, x):
+        r.x.copy_(xi)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for r, s in zip(runs, streams):
+            r.go(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(r.y, w) for r, w in zip(runs, want))
+    graphs = []
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r.go()
+        graphs.append(g)
+    for turn in range(4):
+        for k, r in enumerate(runs):
+            r.x.copy_(x[(k + turn) % 2])
+            r.y.fill_(9)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(r.y, want[(k + turn) % 2]) for k, r in enumerate(runs))
+    assert all(int(r.st) == 0 for r in runs)
