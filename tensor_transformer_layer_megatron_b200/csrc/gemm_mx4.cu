@@ -323,6 +323,430 @@ __global__ void __launch_bounds__(192)
   cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
 }
 
+// ---------------------------------------------------------------------------- CTA pairs
+// Many rows: 256 x 256 tiles on pairs of CTAs (cta_group::2; each CTA holds 128 rows of A, 128 of
+// B and the accumulators of its rows), persistent over the tiles. A stage holds 256 elements of K:
+// 16 KB of A, 16 KB of B and the scales of the CTA's A rows and of all 256 B rows, which both
+// tensor memories need. Operand bytes per multiply-add are those of bf16 at a quarter of the time,
+// so wide tiles matter more than anything else here.
+//
+// Tensor memory: two 256-column accumulators and the scales do not fit 512 columns side by side.
+// The accumulators overlap by 64 columns (0..255 and 192..447): the epilogue reads those first and
+// frees them, and the next tile starts while it goes on with the other 192. Scales take columns
+// 448..: two slots of 24 columns, a slot for 256 (mxfp4) or 128 (nvfp4) elements of K, rewritten
+// once the products that read it have completed.
+//
+// Gated: B is 128 gate rows (CTA 0) and the 128 up rows of the same outputs (CTA 1).
+struct PairArgs {
+  int M, N, kp;
+  int num_m, num_n, m_fast;
+  const float *a_factor, *b_factor;
+  void* C;
+  int c_f32;
+  long long ldc;
+  int width;                // bytes per store that C's (u's) alignment allows: 16, 4 or 2
+  int up_tiles;             // gated: scale tiles of rows before the first up row
+  int act;
+  Mx4Out a;
+  const float* out_factor;
+  __nv_bfloat16* u;
+  long long ldu;
+  int* err;
+};
+
+constexpr int kPairThreads = 320;
+constexpr int kSlotCols = 24;
+constexpr int kAcc1 = 192;     // first column of the second accumulator
+constexpr int kScaleCol = 448;
+constexpr int kStoreBytes = 32 * 144;  // staging of one warp: 32 rows of at most 128 bytes, padded
+
+template <int FMT>
+struct PairCfg {
+  static constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;
+  static constexpr int kStages = FMT == kMxfp4 ? 5 : 4;
+  static constexpr int kScaleBytes = 3 * kTps * 512;
+  static constexpr int kOperandBytes = 2 * 128 * 128;
+  static constexpr int kStageBytes = kOperandBytes + kScaleBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kStoreBytes + 512;
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t bar_cluster,
+                                                 void* dst, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint32_t smem_addr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(scale_desc(smem_addr))
+               : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void tc_mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (FMT == kMxfp4)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// A warp's 32 rows by 32 columns (thread = row) to global memory through its staging buffer, so
+// that consecutive lanes write consecutive bytes of a row. T: bf16 or fp32; width: bytes per lane.
+template <typename T>
+__device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[32], T* base,
+                                            long long ld, int row0, int rows, int col0, int cols,
+                                            int width) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kRow = 32 * (int)sizeof(T) + 16;  // 16-byte accesses of eight rows meet no bank twice
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(stg + lane * kRow + i * 16) =
+          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(stg + lane * kRow + i * 16) =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+  __syncwarp();
+  T* out = base + (long long)row0 * ld + col0;
+  const int nr = min(32, rows - row0), nc = min(32, cols - col0);
+  if (width == 16) {
+    constexpr int kLanes = 32 * sizeof(T) / 16, kElems = 16 / sizeof(T);
+    const int c = (lane % kLanes) * kElems;
+#pragma unroll
+    for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+      const uint4 w = *reinterpret_cast<const uint4*>(stg + r * kRow + c * sizeof(T));
+      if (r < nr) {
+        if (c + kElems <= nc) {
+          *reinterpret_cast<uint4*>(out + (long long)r * ld + c) = w;
+        } else {
+          const T* e = reinterpret_cast<const T*>(stg + r * kRow);
+          for (int i = c; i < nc; ++i) out[(long long)r * ld + i] = e[i];
+        }
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const T e = reinterpret_cast<const T*>(stg + r * kRow)[lane];
+      if (r < nr && lane < nc) out[(long long)r * ld + lane] = e;
+    }
+  }
+  __syncwarp();
+}
+
+template <int FMT, bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmB2,
+                    const __grid_constant__ CUtensorMap tmSA,
+                    const __grid_constant__ CUtensorMap tmSB, const PairArgs g) {
+  using C = PairCfg<FMT>;
+  constexpr int S = C::kStages, kTps = C::kTps;
+  constexpr int kChunks = FMT == kMxfp4 ? 1 : 2;      // scale slots per stage
+  constexpr int kTpc = kTps / kChunks;                // scale tiles per chunk (2)
+  constexpr int kStepsPerChunk = 4 / kChunks;         // products of 64 elements per chunk
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sf = smem + S * C::kOperandBytes;
+  uint8_t* stg = sf + S * C::kScaleBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + 8 * kStoreBytes);
+  uint64_t* empty = full + S;
+  uint64_t* slot_free = empty + S;
+  uint64_t* tfull = slot_free + 2;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* overlap = tempty + 2;
+  uint64_t* drain = overlap + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  const int num_tiles = g.num_m * g.num_n;
+  const int ki = (g.kp + kStageK - 1) / kStageK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&slot_free[b], 1);
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 16);  // the epilogue warps of both CTAs
+    }
+    mbar_init(overlap, 16);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (GATED) tma_prefetch_desc(&tmB2);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA arrive or load
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();  // the operands are the previous kernel's results
+
+  auto tile_m = [&](int t) { return g.m_fast ? t % g.num_m : t / g.num_n; };
+  auto tile_n = [&](int t) { return g.m_fast ? t / g.num_m : t % g.num_n; };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
+      const int m0 = tile_m(tile) * 256 + (int)rank * 128;
+      const int nt = tile_n(tile);
+      const int sb0 = GATED ? nt : 2 * nt, sb1 = GATED ? g.up_tiles + nt : 2 * nt + 1;
+      for (int kt = 0; kt < ki; ++kt) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, g.err, kErrTimeoutProducer, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+        const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+        uint8_t* d = smem + stage * C::kOperandBytes;
+        uint8_t* s = sf + stage * C::kScaleBytes;
+        tma_load_2d_pair(&tmA, fb, d, kt * 128, m0);
+        if (GATED)
+          tma_load_2d_pair(rank ? &tmB2 : &tmB, fb, d + 128 * 128, kt * 128, nt * 128);
+        else
+          tma_load_2d_pair(&tmB, fb, d + 128 * 128, kt * 128, nt * 256 + (int)rank * 128);
+        tma_load_3d_pair(&tmSA, fb, s, 0, kt * kTps, m0 / 128);
+        tma_load_3d_pair(&tmSB, fb, s + kTps * 512, 0, kt * kTps, sb0);
+        tma_load_3d_pair(&tmSB, fb, s + 2 * kTps * 512, 0, kt * kTps, sb1);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // This CTA's loads complete on the leader's barriers: the leader sees all of them land, and
+    // the peer waits for it at the last cluster barrier.
+    if (leader) {
+      for (int i = 1; i <= S; ++i) {
+        int s = stage - i;
+        uint32_t ph = phase;
+        if (s < 0) {
+          s += S;
+          ph ^= 1;
+        }
+        mbar_wait(&full[s], ph, g.err, kErrTimeoutDrain, nullptr);
+      }
+    }
+  } else if (leader && warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ products (leader only)
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, acc_phase = 0, slot_phase = 0, ov_phase = 0;
+    bool ok = true, first = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
+      if (!mbar_wait(&tempty[acc], acc_phase ^ 1, g.err, kErrTimeoutMma, abort_flag)) break;
+      if (!first) {  // the previous tile's share of the common columns has been read
+        if (!mbar_wait(overlap, ov_phase, g.err, kErrTimeoutMma, abort_flag)) break;
+        ov_phase ^= 1;
+      }
+      first = false;
+      tc_fence_after();
+      const uint32_t d = tmem + (acc ? kAcc1 : 0);
+      for (int kt = 0; kt < ki; ++kt) {
+        if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int steps = min(4, (g.kp - kt * kStageK) / 64);
+        const uint32_t aa = smem_u32(smem + stage * C::kOperandBytes), ba = aa + 128 * 128;
+        const uint32_t ss = smem_u32(sf + stage * C::kScaleBytes);
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (ch * kStepsPerChunk >= steps) break;
+          if (!mbar_wait(&slot_free[slot], slot_phase ^ 1, g.err, kErrTimeoutMma, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sc = tmem + kScaleCol + slot * kSlotCols;
+#pragma unroll
+          for (int t = 0; t < kTpc; ++t) {
+            tc_cp_scales_pair(sc + t * 4, ss + (ch * kTpc + t) * 512);
+            tc_cp_scales_pair(sc + kTpc * 4 + t * 8, ss + (kTps + ch * kTpc + t) * 512);
+            tc_cp_scales_pair(sc + kTpc * 4 + t * 8 + 4, ss + (2 * kTps + ch * kTpc + t) * 512);
+          }
+#pragma unroll
+          for (int j = 0; j < kStepsPerChunk; ++j) {
+            const int k = ch * kStepsPerChunk + j;
+            if (k >= steps) break;
+            const int t = FMT == kMxfp4 ? j >> 1 : j;
+            const uint32_t id = FMT == kMxfp4 ? (uint32_t)(j & 1) * 2 : 0u;
+            tc_mma_mx4_pair<FMT>(d, smem_desc_sw128(aa + k * 32, 16, 1024),
+                                 smem_desc_sw128(ba + k * 32, 16, 1024),
+                                 idesc_mx4<FMT>(256, 256, id), sc + t * 4, sc + kTpc * 4 + t * 8,
+                                 (kt > 0 || k > 0) ? 1u : 0u);
+          }
+          tc_commit_pair(&slot_free[slot]);
+          if (++slot == 2) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&empty[stage], 0x3);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      tc_commit_pair_mc(&tfull[acc], 0x3);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    tc_commit_pair(drain);
+    mbar_wait(drain, 0, g.err, kErrTimeoutDrain, nullptr);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int ew = warp & 3, set = (warp - 2) >> 2;
+    uint8_t* my = stg + (warp - 2) * kStoreBytes;
+    const float f = (g.a_factor ? g.a_factor[1] : 1.f) * (g.b_factor ? g.b_factor[1] : 1.f);
+    const float inv_f =
+        GATED && FMT == kNvfp4 ? 1.0f / (g.out_factor ? g.out_factor[1] : 1.f) : 1.f;
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t overlap0 = mapa_shared(smem_u32(overlap), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = pair; tile < num_tiles; tile += num_pairs) {
+      const int row0 = tile_m(tile) * 256 + (int)rank * 128 + ew * 32;
+      const int row = row0 + lane;
+      const int nt = tile_n(tile);
+      if (!mbar_wait(&tfull[acc], acc_phase, g.err, kErrTimeoutEpilogue, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t t0 = tmem + (acc ? kAcc1 : 0) + ((uint32_t)(ew * 32) << 16);
+      if constexpr (!GATED) {
+        // 32-column chunks; the first one lies in the columns common to both accumulators (6, 7
+        // of the first, 0, 1 of the second)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int c = acc ? (i == 0 ? set : 1 + 3 * set + i) : (i == 0 ? 6 + set : 3 * set + i - 1);
+          float v[32];
+          tmem_ld_32x32b_x32(t0 + c * 32, v);
+          if (i == 0 || i == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(i == 0 ? overlap0 : tempty0 + acc * 8);
+          }
+          const int col0 = nt * 256 + c * 32;
+          if (col0 < g.N && row0 < g.M) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= f;
+            if (g.c_f32)
+              store_block(my, v, static_cast<float*>(g.C), g.ldc, row0, g.M, col0, g.N, g.width);
+            else
+              store_block(my, v, static_cast<__nv_bfloat16*>(g.C), g.ldc, row0, g.M, col0, g.N,
+                          g.width);
+          }
+        }
+      } else {
+        // gate chunk c and up chunk c + 4 of the same outputs; c = 2, 3 first in the first
+        // accumulator (their up chunks are common columns), 0, 1 first in the second
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int c = ((acc ? i : 1 - i) * 2) + set;
+          float v[32], w[32];
+          tmem_ld_32x32b_x32(t0 + c * 32, v);
+          tmem_ld_32x32b_x32(t0 + 128 + c * 32, w);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(i == 0 ? overlap0 : tempty0 + acc * 8);
+          const int col0 = nt * 128 + c * 32;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            v[k] *= f;
+            w[k] *= f;
+          }
+          if (g.u && row0 < g.M) {
+            if (col0 < g.N) {
+              store_block(my, v, g.u, g.ldu, row0, g.M, col0, g.N, g.width);
+              store_block(my, w, g.u + g.N, g.ldu, row0, g.M, col0, g.N, g.width);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float h, dh;
+            gate_and_grad(v[k], g.act, h, dh);
+            v[k] = col0 + k < g.N ? h * w[k] : 0.f;  // columns behind the last are zeros
+          }
+          constexpr int B = Mx4Fmt<FMT>::kBlock;
+          uint32_t codes[4], bytes = 0;
+#pragma unroll
+          for (int b = 0; b < 32 / B; ++b) {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int k = 0; k < B; ++k) mx = max(mx, abs_bits(v[b * B + k]));
+            const Mx4Block q = mx4_block<FMT>(mx, inv_f);
+            bytes |= q.byte << (8 * b);
+#pragma unroll
+            for (int k = 0; k < B / 8; ++k) {
+              float e[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) e[j] = v[b * B + k * 8 + j];
+              codes[b * (B / 8) + k] = mx4_codes8<FMT>(e, q, inv_f);
+            }
+          }
+          if (row < g.M) {
+            *reinterpret_cast<uint4*>(g.a.codes + ((long long)row * g.a.ld + col0) / 2) =
+                make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            uint8_t* sp = g.a.scales + mx4_scale_off<FMT>(row, col0 / B, g.a.ld);
+            if constexpr (FMT == kMxfp4)
+              *sp = (uint8_t)bytes;
+            else
+              *reinterpret_cast<uint16_t*>(sp) = (uint16_t)bytes;
+          }
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still touch its barriers or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ---------------------------------------------------------------------------- host side
 bool map_codes(CUtensorMap* m, const uint8_t* codes, int rows, int kp, long long ld, int box_rows) {
   return make_tensor_map_u8_2d(m, codes, (uint64_t)kp / 2, (uint64_t)rows, (uint64_t)ld / 2,
@@ -399,14 +823,63 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, tp, tp2, tq, a);
 }
 
+int store_width(const void* p, long long ld, int esz) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0 ? 16 : esz;
+}
+
+template <int FMT, bool GATED>
+cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
+  using C = PairCfg<FMT>;
+  const int kp = (g.K + 127) & ~127;
+  const int up0 = (g.N + 127) & ~127;
+  CUtensorMap ta, tb, tb2, tsa, tsb;
+  const int b_rows = GATED ? 2 * up0 : g.N;
+  if (!map_codes(&ta, g.A.codes, g.M, kp, g.A.ld, 128) ||
+      !map_codes(&tb, g.B.codes, g.N, kp, g.B.ld, 128) ||
+      !map_codes(&tb2, g.B.codes + (GATED ? up0 * g.B.ld / 2 : 0), g.N, kp, g.B.ld, 128) ||
+      !make_tensor_map_tiles(&tsa, g.A.scales, kp / Mx4Fmt<FMT>::kTileCols, (g.M + 127) / 128,
+                             g.A.ld / Mx4Fmt<FMT>::kTileCols, C::kTps) ||
+      !make_tensor_map_tiles(&tsb, g.B.scales, kp / Mx4Fmt<FMT>::kTileCols, (b_rows + 127) / 128,
+                             g.B.ld / Mx4Fmt<FMT>::kTileCols, C::kTps))
+    return cudaErrorInvalidValue;
+  PairArgs a = {};
+  a.M = g.M; a.N = g.N; a.kp = kp;
+  a.num_m = (g.M + 255) / 256;
+  a.num_n = GATED ? up0 / 128 : (g.N + 255) / 256;
+  a.m_fast = g.M <= b_rows;  // the operand that every wave sweeps again is the smaller one
+  a.a_factor = g.a_factor; a.b_factor = g.b_factor;
+  a.C = g.C; a.c_f32 = g.c_f32; a.ldc = g.ldc;
+  a.up_tiles = up0 / 128;
+  a.act = g.act; a.a = g.a; a.out_factor = g.out_factor;
+  a.u = static_cast<__nv_bfloat16*>(g.u); a.ldu = g.ldu;
+  if (GATED)
+    a.width = (g.N % 8) ? 2 : store_width(g.u, g.ldu, 2);
+  else
+    a.width = store_width(g.C, g.ldc, g.c_f32 ? 4 : 2);
+  a.err = g.err;
+  auto kern = mx4_pair_kernel<FMT, GATED>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int tiles = a.num_m * a.num_n;
+  const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  return launch_kernel(true, kern, dim3(2 * pairs), dim3(kPairThreads), (size_t)C::kSmem, s, ta, tb,
+                       tb2, tsa, tsb, a);
+}
+
+template <int FMT, bool GATED>
+cudaError_t launch_any(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
+  if (g.M > 256) return launch_pair<FMT, GATED>(g, num_sms, s);
+  return launch_skinny<FMT, GATED>(g, num_sms, s);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_mx4(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   if (g.fmt == kMxfp4)
-    return g.gated ? launch_skinny<kMxfp4, true>(g, num_sms, s)
-                   : launch_skinny<kMxfp4, false>(g, num_sms, s);
-  return g.gated ? launch_skinny<kNvfp4, true>(g, num_sms, s)
-                 : launch_skinny<kNvfp4, false>(g, num_sms, s);
+    return g.gated ? launch_any<kMxfp4, true>(g, num_sms, s)
+                   : launch_any<kMxfp4, false>(g, num_sms, s);
+  return g.gated ? launch_any<kNvfp4, true>(g, num_sms, s)
+                 : launch_any<kNvfp4, false>(g, num_sms, s);
 }
 
 }  // namespace mgt

@@ -135,6 +135,10 @@ bool make_tensor_map_i32_3d(CUtensorMap* m, const void* base, const uint64_t dim
 // zero fill out of bounds).
 bool make_tensor_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                            uint64_t ld, uint32_t box_rows);
+// Tensor map over 512-byte tiles [rows][ld tiles], `tiles` of each row inside; box one row by
+// box_tiles tiles, unswizzled, zero fill out of bounds.
+bool make_tensor_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t rows,
+                           uint64_t ld, uint32_t box_tiles);
 
 // tcgen05 / TMA GEMM for bf16 operands (fp32 accumulate in tensor memory).
 // Builds the tensor maps from the pointers in `args` (A, B, strides) and launches a persistent
