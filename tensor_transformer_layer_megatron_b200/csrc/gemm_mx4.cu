@@ -47,23 +47,37 @@ __device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t id) {
   return (1u << 7) | (1u << 10) | (id << 4) | ((uint32_t)(N >> 3) << 17) |
          (FMT == kMxfp4 ? 1u << 23 : 0u) | ((uint32_t)(M >> 7) << 27) | (id << 29);
 }
-template <int FMT>
-__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// a, b: low words of the operands' descriptors (start address >> 4, leading offset 1); the high
+// word, the same for every K-major tile with 128-byte swizzle, joins them here.
+template <int FMT, int GROUP>
+__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t sa, uint32_t sb, uint32_t accumulate) {
-  if constexpr (FMT == kMxfp4)
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+  constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+#define MX4_MMA(group, kind)                                                                  \
+  asm volatile("{ .reg .pred p; .reg .b64 da, db; setp.ne.b32 p, %6, 0;\n\t"                  \
+               "mov.b64 da, {%1, %7}; mov.b64 db, {%2, %7};\n\t"                              \
+               "tcgen05.mma.cta_group::" group ".kind::" kind                                 \
+               " [%0], da, db, %3, [%4], [%5], p; }" ::"r"(d),                                \
+               "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "n"(kHigh)      \
+               : "memory")
+  if constexpr (FMT == kMxfp4 && GROUP == 1)
+    MX4_MMA("1", "mxf4.block_scale.scale_vec::2X");
+  else if constexpr (FMT == kMxfp4)
+    MX4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  else if constexpr (GROUP == 1)
+    MX4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
   else
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
-        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+    MX4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+#undef MX4_MMA
+}
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFF) | (1u << 16);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
 }
 
 constexpr int kStageK = 256;          // elements of K per stage: 128 bytes of a row
@@ -79,6 +93,7 @@ constexpr int kPBytes = kPRows * 128;
 struct SkinnyArgs {
   int M, N, kp;                 // tokens, weight rows (per matrix), K rounded up to 128
   int bnq, stages, tmem_cols;
+  int vec;                      // C (u) takes stores of four elements
   const uint8_t* p_scales;
   const uint8_t* p2_scales;
   long long p_ld;
@@ -96,10 +111,32 @@ struct SkinnyArgs {
   int* err;
 };
 
-__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
   return v;
+}
+
+// Up to four consecutive outputs; vec: the address allows one store of all four.
+__device__ __forceinline__ void store4(float* o, const float (&v)[4], int n, int vec) {
+  if (vec && n >= 4) {
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) o[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* o, const float (&v)[4], int n, int vec) {
+  if (vec && n >= 4) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) o[i] = __float2bfloat16_rn(v[i]);
+  }
 }
 
 template <int FMT, bool GATED>
@@ -196,49 +233,62 @@ __global__ void __launch_bounds__(192)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      const uint32_t sf_cols = (uint32_t)(NM + groups) * kTps * 4;
-      for (int kt = k_begin; kt < k_end; ++kt) {
-        if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) break;
-        tc_fence_after();
-        const int n = min(kTps, k_tiles - kt * kTps);
-        const int steps = min(4, (g.kp - kt * kStageK) / 64);
-        // Each stage has scale columns of its own: they are rewritten only after the producer
-        // has seen the products of the stage's last use complete.
-        const uint32_t sc = tmem + NM * acc_cols + stage * sf_cols;
-        const uint32_t ss = smem_u32(sf + stage * sf_bytes);
-        for (int t = 0; t < n; ++t) {
+    // The whole warp runs the loop and one elected lane issues: descriptors and addresses then
+    // are warp-uniform values. Issued from a lone thread's registers, a stage's products and
+    // scale copies took longer to issue than to run.
+    const bool one = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    const uint32_t sf_cols = (uint32_t)(NM + groups) * kTps * 4;
+    for (int kt = k_begin; kt < k_end; ++kt) {
+      if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) break;
+      tc_fence_after();
+      const int n = min(kTps, k_tiles - kt * kTps);
+      const int steps = min(4, (g.kp - kt * kStageK) / 64);
+      // Each stage has scale columns of its own: they are rewritten only after the producer
+      // has seen the products of the stage's last use complete.
+      const uint32_t sc = tm + NM * acc_cols + stage * sf_cols;
+      const uint32_t ss = smem_u32(sf + stage * sf_bytes);
+      const uint32_t pa = desc_low(smem_u32(smem + stage * stage_bytes));
+      const uint32_t qa = pa + NM * (kPBytes >> 4);
+      if (one) {
 #pragma unroll
-          for (int m = 0; m < NM; ++m)
-            tc_cp_scales(sc + (m * kTps + t) * 4, ss + (m * kTps + t) * 512);
-          for (int q = 0; q < groups; ++q)
-            tc_cp_scales(sc + (NM * kTps + t * groups + q) * 4, ss + ((NM + q) * kTps + t) * 512);
+        for (int t = 0; t < kTps; ++t) {
+          if (t < n) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              tc_cp_scales(sc + (m * kTps + t) * 4, ss + (m * kTps + t) * 512);
+            tc_cp_scales(sc + (NM * kTps + t * groups) * 4, ss + (NM * kTps + t) * 512);
+            if (groups == 2)
+              tc_cp_scales(sc + (NM * kTps + t * 2 + 1) * 4, ss + ((NM + 1) * kTps + t) * 512);
+          }
         }
-        const uint32_t pa = smem_u32(smem + stage * stage_bytes);
-        const uint32_t qa = pa + NM * kPBytes;
-        for (int k = 0; k < steps; ++k) {
-          const int t = FMT == kMxfp4 ? k >> 1 : k;
-          const uint32_t id = FMT == kMxfp4 ? (uint32_t)(k & 1) * 2 : 0u;
-          const uint32_t idesc = idesc_mx4<FMT>(kPRows, g.bnq, id);
-          const uint64_t qd = smem_desc_sw128(qa + k * 32, 16, 1024);
 #pragma unroll
-          for (int m = 0; m < NM; ++m)
-            tc_mma_mx4<FMT>(tmem + m * acc_cols, smem_desc_sw128(pa + m * kPBytes + k * 32, 16, 1024),
-                            qd, idesc, sc + (m * kTps + t) * 4, sc + (NM * kTps + t * groups) * 4,
-                            (kt > k_begin || k > 0) ? 1u : 0u);
+        for (int k = 0; k < 4; ++k) {
+          if (k < steps) {
+            const int t = FMT == kMxfp4 ? k >> 1 : k;
+            const uint32_t id = FMT == kMxfp4 ? (uint32_t)(k & 1) * 2 : 0u;
+            const uint32_t idesc = idesc_mx4<FMT>(kPRows, g.bnq, id);
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              tc_mma_mx4<FMT, 1>(tm + m * acc_cols, pa + m * (kPBytes >> 4) + 2 * k, qa + 2 * k,
+                                 idesc, sc + (m * kTps + t) * 4,
+                                 sc + (NM * kTps + t * groups) * 4,
+                                 k > 0 ? 1u : (uint32_t)(kt - k_begin));
+          }
         }
         tc_commit(&empty[stage]);
-        if (++stage == g.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
-      tc_commit(tfull);
-      mbar_wait(tfull, 0, g.err, kErrTimeoutDrain, nullptr);
+      __syncwarp();
+      if (++stage == g.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
+    if (one) tc_commit(tfull);
     __syncwarp();
+    mbar_wait(tfull, 0, g.err, kErrTimeoutDrain, nullptr);
   }
 
   // Partial tiles [matrix][token][128] in the operand stages' memory: all copies into it have
@@ -273,49 +323,65 @@ __global__ void __launch_bounds__(192)
     tmem_dealloc(tmem, g.tmem_cols);
   }
   if (epi && ok) {
+    // A warp takes a token of its CTA's share at a time, a lane four neighbouring weight rows.
     const float f = (g.p_factor ? g.p_factor[1] : 1.f) * (g.q_factor ? g.q_factor[1] : 1.f);
     const int tokens = min(g.bnq, g.M - q0);
-    const uint32_t mine = smem_u32(part + p);
+    const uint32_t mine = smem_u32(part + lane * 4);
+    const int col = p0 + lane * 4;
     const float inv_f = GATED && FMT == kNvfp4 ? 1.0f / (g.out_factor ? g.out_factor[1] : 1.f) : 1.f;
-#pragma unroll 1
-    for (int t = (int)rank; t < tokens; t += (int)csize) {
-      float v[NM];
+#pragma unroll 2
+    for (int t = (int)rank * 4 + (warp - 2); t < tokens; t += 4 * (int)csize) {
+      float v[NM][4];
 #pragma unroll
-      for (int m = 0; m < NM; ++m) v[m] = 0.f;
-      for (uint32_t r = 0; r < csize; ++r)
+      for (int m = 0; m < NM; ++m) {
+        v[m][0] = v[m][1] = v[m][2] = v[m][3] = 0.f;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-          v[m] += ld_dsmem(mapa_shared(mine + (uint32_t)((m * g.bnq + t) * kPRows * 4), r));
+        for (uint32_t r = 0; r < 8; ++r) {
+          if (r < csize) {
+            const float4 w =
+                ld_dsmem4(mapa_shared(mine + (uint32_t)((m * g.bnq + t) * kPRows * 4), r));
+            v[m][0] += w.x;
+            v[m][1] += w.y;
+            v[m][2] += w.z;
+            v[m][3] += w.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[m][i] *= f;
+      }
       const long long row = q0 + t;
-      const int col = p0 + p;
       if constexpr (!GATED) {
-        if (col < g.N) {
-          if (g.c_f32)
-            static_cast<float*>(g.C)[row * g.ldc + col] = v[0] * f;
-          else
-            static_cast<__nv_bfloat16*>(g.C)[row * g.ldc + col] = __float2bfloat16_rn(v[0] * f);
-        }
+        if (g.c_f32)
+          store4(static_cast<float*>(g.C) + row * g.ldc + col, v[0], g.N - col, g.vec);
+        else
+          store4(static_cast<__nv_bfloat16*>(g.C) + row * g.ldc + col, v[0], g.N - col, g.vec);
       } else {
-        const float gate = v[0] * f, up = v[NM - 1] * f;
-        if (g.u && col < g.N) {
-          g.u[row * g.ldu + col] = __float2bfloat16_rn(gate);
-          g.u[row * g.ldu + g.N + col] = __float2bfloat16_rn(up);
+        if (g.u) {
+          store4(g.u + row * g.ldu + col, v[0], g.N - col, g.vec);
+          store4(g.u + row * g.ldu + g.N + col, v[NM - 1], g.N - col, g.vec);
         }
-        float h, dh;
-        gate_and_grad(gate, g.act, h, dh);
-        const float a = col < g.N ? h * up : 0.f;  // columns behind the last are zeros
-        constexpr int B = Mx4Fmt<FMT>::kBlock;
-        uint32_t mx = abs_bits(a);
+        float a[4];
+        uint32_t mx = 0;
 #pragma unroll
-        for (int o = B / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int i = 0; i < 4; ++i) {
+          float h, dh;
+          gate_and_grad(v[0][i], g.act, h, dh);
+          a[i] = col + i < g.N ? h * v[NM - 1][i] : 0.f;  // columns behind the last are zeros
+          mx = max(mx, abs_bits(a[i]));
+        }
+        constexpr int B = Mx4Fmt<FMT>::kBlock;
+#pragma unroll
+        for (int o = B / 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const Mx4Block q = mx4_block<FMT>(mx, inv_f);
-        const float x = mx4_scaled<FMT>(a, q, inv_f);
         float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __shfl_down_sync(0xffffffffu, x, i);
-        if (lane % 8 == 0)
-          *reinterpret_cast<uint32_t*>(g.a.codes + (row * g.a.ld + col) / 2) = e2m1x8(w) & q.mask;
-        if (lane % B == 0)
+        for (int i = 0; i < 4; ++i) {
+          w[i] = mx4_scaled<FMT>(a[i], q, inv_f);
+          w[i + 4] = 0.f;
+        }
+        *reinterpret_cast<uint16_t*>(g.a.codes + (row * g.a.ld + col) / 2) =
+            (uint16_t)(e2m1x8(w) & q.mask);
+        if (col % B == 0)
           g.a.scales[mx4_scale_off<FMT>(row, col / B, g.a.ld)] = (uint8_t)q.byte;
       }
     }
@@ -383,25 +449,6 @@ __device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint32_t smem_
                "l"(scale_desc(smem_addr))
                : "memory");
 }
-template <int FMT>
-__device__ __forceinline__ void tc_mma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t sa, uint32_t sb, uint32_t accumulate) {
-  if constexpr (FMT == kMxfp4)
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
-        " [%0], %1, %2, %3, [%4], [%5], p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-}
-
 // A warp's 32 rows by 32 columns (thread = row) to global memory through its staging buffer, so
 // that consecutive lanes write consecutive bytes of a row. T: bf16 or fp32; width: bytes per lane.
 template <typename T>
@@ -561,8 +608,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         mbar_wait(&full[s], ph, g.err, kErrTimeoutDrain, nullptr);
       }
     }
-  } else if (leader && warp == 1 && lane == 0) {
+  } else if (leader && warp == 1) {
     // ------------------------------------------------------------ products (leader only)
+    // The whole warp runs the loop and one elected lane issues, so that descriptors and
+    // addresses are warp-uniform values: issued from a lone thread's registers, four products took
+    // longer to issue than to run.
+    const bool one = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     int stage = 0, acc = 0, slot = 0;
     uint32_t phase = 0, acc_phase = 0, slot_phase = 0, ov_phase = 0;
     bool ok = true, first = true;
@@ -573,15 +625,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ov_phase ^= 1;
       }
       first = false;
-      tc_fence_after();
-      const uint32_t d = tmem + (acc ? kAcc1 : 0);
+      const uint32_t d = tm + (acc ? kAcc1 : 0);
       for (int kt = 0; kt < ki; ++kt) {
         if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) {
           ok = false;
           break;
         }
         const int steps = min(4, (g.kp - kt * kStageK) / 64);
-        const uint32_t aa = smem_u32(smem + stage * C::kOperandBytes), ba = aa + 128 * 128;
+        const uint32_t aa = desc_low(smem_u32(smem + stage * C::kOperandBytes));
+        const uint32_t ba = aa + (128 * 128 >> 4);
         const uint32_t ss = smem_u32(sf + stage * C::kScaleBytes);
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch) {
@@ -591,45 +643,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sc = tmem + kScaleCol + slot * kSlotCols;
+          const uint32_t sc = tm + kScaleCol + slot * kSlotCols;
+          if (one) {
 #pragma unroll
-          for (int t = 0; t < kTpc; ++t) {
-            tc_cp_scales_pair(sc + t * 4, ss + (ch * kTpc + t) * 512);
-            tc_cp_scales_pair(sc + kTpc * 4 + t * 8, ss + (kTps + ch * kTpc + t) * 512);
-            tc_cp_scales_pair(sc + kTpc * 4 + t * 8 + 4, ss + (2 * kTps + ch * kTpc + t) * 512);
-          }
+            for (int t = 0; t < kTpc; ++t) {
+              tc_cp_scales_pair(sc + t * 4, ss + (ch * kTpc + t) * 512);
+              tc_cp_scales_pair(sc + kTpc * 4 + t * 8, ss + (kTps + ch * kTpc + t) * 512);
+              tc_cp_scales_pair(sc + kTpc * 4 + t * 8 + 4, ss + (2 * kTps + ch * kTpc + t) * 512);
+            }
 #pragma unroll
-          for (int j = 0; j < kStepsPerChunk; ++j) {
-            const int k = ch * kStepsPerChunk + j;
-            if (k >= steps) break;
-            const int t = FMT == kMxfp4 ? j >> 1 : j;
-            const uint32_t id = FMT == kMxfp4 ? (uint32_t)(j & 1) * 2 : 0u;
-            tc_mma_mx4_pair<FMT>(d, smem_desc_sw128(aa + k * 32, 16, 1024),
-                                 smem_desc_sw128(ba + k * 32, 16, 1024),
-                                 idesc_mx4<FMT>(256, 256, id), sc + t * 4, sc + kTpc * 4 + t * 8,
-                                 (kt > 0 || k > 0) ? 1u : 0u);
+            for (int j = 0; j < kStepsPerChunk; ++j) {
+              const int k = ch * kStepsPerChunk + j;
+              if (k < steps) {
+                const int t = FMT == kMxfp4 ? j >> 1 : j;
+                const uint32_t id = FMT == kMxfp4 ? (uint32_t)(j & 1) * 2 : 0u;
+                tc_mma_mx4<FMT, 2>(d, aa + 2 * k, ba + 2 * k, idesc_mx4<FMT>(256, 256, id),
+                                   sc + t * 4, sc + kTpc * 4 + t * 8, k > 0 ? 1u : (uint32_t)kt);
+              }
+            }
+            tc_commit_pair(&slot_free[slot]);
           }
-          tc_commit_pair(&slot_free[slot]);
+          __syncwarp();
           if (++slot == 2) {
             slot = 0;
             slot_phase ^= 1;
           }
         }
         if (!ok) break;
-        tc_commit_pair_mc(&empty[stage], 0x3);
+        if (one) tc_commit_pair_mc(&empty[stage], 0x3);
+        __syncwarp();
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      tc_commit_pair_mc(&tfull[acc], 0x3);
+      if (one) tc_commit_pair_mc(&tfull[acc], 0x3);
+      __syncwarp();
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
       }
     }
-    tc_commit_pair(drain);
+    if (one) tc_commit_pair(drain);
+    __syncwarp();
     mbar_wait(drain, 0, g.err, kErrTimeoutDrain, nullptr);
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -753,6 +810,10 @@ bool map_codes(CUtensorMap* m, const uint8_t* codes, int rows, int kp, long long
                                (uint32_t)box_rows);
 }
 
+bool store_vec4(const void* p, long long ld, int esz) {
+  return (reinterpret_cast<uintptr_t>(p) & (4 * esz - 1)) == 0 && ld % 4 == 0;
+}
+
 template <int FMT, bool GATED>
 cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   constexpr int NM = GATED ? 2 : 1;
@@ -799,6 +860,8 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   a.C = g.C; a.c_f32 = g.c_f32; a.ldc = g.ldc;
   a.act = g.act; a.a = g.a; a.out_factor = g.out_factor;
   a.u = static_cast<__nv_bfloat16*>(g.u); a.ldu = g.ldu;
+  a.vec = GATED ? g.N % 4 == 0 && store_vec4(g.u, g.ldu, 2)
+                : store_vec4(g.C, g.ldc, g.c_f32 ? 4 : 2);
   a.err = g.err;
 
   auto kern = mx4_skinny_kernel<FMT, GATED>;
