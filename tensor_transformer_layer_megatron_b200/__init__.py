@@ -14,6 +14,18 @@ __all__ = ["Layer", "MgtError", "load_library", "gemm_bf16", "layernorm_bwd_noal
            "PARAM_ORDER", "lib_path", "Mx4", "mx4_tensor_factor", "mx4_quantize",
            "mx4_dequantize", "gemm_mx4", "gemm_mx4_gated", "mx4_gated_bwd"]
 
+# The 4-bit operators live in mx4.py (which imports torch) and are loaded at first use.
+_MX4 = ("Mx4", "mx4_tensor_factor", "mx4_quantize", "mx4_dequantize", "gemm_mx4",
+        "gemm_mx4_gated", "mx4_gated_bwd")
+
+
+def __getattr__(name):
+    if name in _MX4:
+        from . import mx4
+        globals().update({n: getattr(mx4, n) for n in _MX4})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libmgt.so")
 
@@ -61,12 +73,6 @@ class _KernelStat(ctypes.Structure):
                 ("ms", ctypes.c_double), ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
 
 
-class _Mx4Operand(ctypes.Structure):
-    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
-                ("ld", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
-                ("factor", ctypes.c_void_p)]
-
-
 _LIB = None
 
 
@@ -104,7 +110,7 @@ def load_library():
     i64 = ctypes.c_int64
     lib.mgt_mx4_sizes.argtypes = [i32, i32, i32, ctypes.POINTER(i64), ctypes.POINTER(sz),
                                   ctypes.POINTER(sz)]
-    # operands go by address (ctypes.addressof of a _Mx4Operand that the caller keeps)
+    # operands go by address (mx4.py keeps a struct per operand)
     lib.mgt_mx4_tensor_factor.argtypes = [i32, i32, i32, vp, i64, vp, vp]
     lib.mgt_mx4_quantize.argtypes = [i32, vp, i64, vp, vp, vp]
     lib.mgt_mx4_dequantize.argtypes = [vp, i32, vp, i64, vp]
@@ -418,205 +424,6 @@ def gemm_fp8(A, B, a_scales, b_scales, C, M, N, K, lda, ldb, ldc, status, stream
     _check(lib.mgt_gemm_fp8(M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(a_scales),
                             _ptr(b_scales), _ptr(C), 0 if C.dtype == torch.float32 else 1, ldc,
                             _ptr(status), _stream_handle(stream)), "mgt_gemm_fp8")
-
-
-MX4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
-ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
-
-
-def _up128(n):
-    return (n + 127) // 128 * 128
-
-
-class Mx4:
-    """A microscaled 4-bit operand of `rows` by `cols` (see mgt_mx4 in include/mgt_layer.h):
-    device buffers for its codes [rows, ld / 2] and scale tiles, both uint8, and for "nvfp4" its
-    factor {amax, f}, two fp32 on the device. Buffers are allocated (f = 1), or given: codes
-    with rows of ld / 2 contiguous bytes, `scales` with room for whole tiles of 128 rows."""
-
-    def __init__(self, fmt, rows, cols, device="cuda", codes=None, scales=None, factor=None):
-        import torch
-        if fmt not in MX4_FORMATS:
-            raise ValueError("format must be one of %s" % sorted(MX4_FORMATS))
-        rows, cols = int(rows), int(cols)
-        if rows < 1 or cols < 1:
-            raise ValueError("an operand has at least one row and one column")
-        block = 32 if fmt == "mxfp4" else 16
-        if codes is None:
-            codes = torch.empty(rows, _up128(cols) // 2, dtype=torch.uint8, device=device)
-        if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.shape[0] < rows or \
-                codes.stride(1) != 1 or (codes.shape[0] > 1 and
-                                         codes.stride(0) != codes.shape[1]):
-            raise TypeError("codes must be contiguous uint8 [rows, ld / 2]")
-        self.ld = 2 * codes.shape[1]
-        if self.ld % 128 or self.ld < _up128(cols):
-            raise ValueError("ld must be a multiple of 128 that holds all columns")
-        need = _up128(rows) * self.ld // block
-        if scales is None:
-            scales = torch.empty(need, dtype=torch.uint8, device=codes.device)
-        if scales.dtype != torch.uint8 or not scales.is_contiguous():
-            raise TypeError("scales must be contiguous uint8")
-        if scales.numel() < need:
-            raise ValueError("scales need %d bytes" % need)
-        if fmt == "nvfp4" and factor is None:
-            factor = torch.ones(2, dtype=torch.float32, device=codes.device)
-        if factor is not None and (factor.dtype != torch.float32 or factor.numel() < 2 or
-                                   not factor.is_contiguous()):
-            raise TypeError("factor must be two contiguous float32")
-        for t in (scales, factor):
-            if t is not None and t.device != codes.device:
-                raise ValueError("codes, scales and factor must be on one device")
-        self.fmt, self.rows, self.cols = fmt, rows, cols
-        self.codes, self.scales, self.factor = codes, scales, factor
-        self._bind(0, 0)
-
-    def _bind(self, row, col):
-        block = 32 if self.fmt == "mxfp4" else 16
-        self._row, self._col = row, col
-        self._c = _Mx4Operand(
-            MX4_FORMATS[self.fmt], self.rows, self.cols, self.ld,
-            self.codes.data_ptr() + (row * self.ld + col) // 2,
-            self.scales.data_ptr() + 512 * (row // 128 * (self.ld // (4 * block)) +
-                                            col // (4 * block)),
-            None if self.factor is None else self.factor.data_ptr())
-        self._addr = ctypes.addressof(self._c)
-
-    def part(self, row, rows, col, cols):
-        """The operand of rows row .. row + rows - 1 and columns col .. col + cols - 1 of this
-        one, in the same buffers; row and col are multiples of 128."""
-        if row % 128 or col % 128 or row < 0 or col < 0 or rows < 1 or cols < 1 or \
-                row + rows > self.rows or _up128(col + cols) > _up128(self.cols):
-            raise ValueError("a part starts at multiples of 128 and lies inside the operand")
-        p = object.__new__(Mx4)
-        p.fmt, p.rows, p.cols, p.ld = self.fmt, int(rows), int(cols), self.ld
-        p.codes, p.scales, p.factor = self.codes, self.scales, self.factor
-        p._bind(self._row + row, self._col + col)
-        return p
-
-    def rows_view(self, row, rows):
-        """The operand of rows row .. row + rows - 1 (row a multiple of 128), all columns."""
-        return self.part(row, rows, 0, self.cols)
-
-
-def _matrix(t, name):
-    """(dtype code, row stride) of a 2-D fp32 or bf16 tensor with contiguous rows."""
-    import torch
-    if t.dtype == torch.bfloat16:
-        code = 1
-    elif t.dtype == torch.float32:
-        code = 0
-    else:
-        raise TypeError("%s must be float32 or bfloat16" % name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise TypeError("%s must be 2-D with contiguous rows" % name)
-    return code, t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _device_stream(device, stream):
-    """(guard, handle): launches go to the tensors' device, on its current stream unless one is
-    given."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream belongs to another device than the tensors")
-    return (torch.cuda.device(device),
-            (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
-
-
-def _mx4_call(name, device, stream, others, *args):
-    for t in others:
-        if t is not None and (t.codes.device if isinstance(t, Mx4) else t.device) != device:
-            raise ValueError("all tensors must be on one device")
-    guard, handle = _device_stream(device, stream)
-    with guard:
-        _check(getattr(load_library(), name)(*args, handle), name)
-
-
-def _check_status(status):
-    import torch
-    if status.dtype != torch.int32:
-        raise TypeError("status must be an int32 device word")
-
-
-def _addr(q):
-    return None if q is None else q._addr
-
-
-def mx4_tensor_factor(x, factor, stream=None):
-    """factor = {amax, f} of a 2-D tensor for "nvfp4" (see mgt_mx4_tensor_factor)."""
-    import torch
-    code, ld = _matrix(x, "x")
-    if factor.dtype != torch.float32 or factor.numel() < 2 or not factor.is_contiguous():
-        raise TypeError("factor must be two contiguous float32")
-    _mx4_call("mgt_mx4_tensor_factor", x.device, stream, (factor,), code, x.shape[0], x.shape[1],
-              _ptr(x), ld, _ptr(factor))
-
-
-def mx4_quantize(x, q=None, qt=None, stream=None):
-    """Quantise x [rows, cols] (fp32 or bf16) into q and / or, transposed, into qt (see
-    mgt_mx4_quantize)."""
-    code, ld = _matrix(x, "x")
-    if (q is not None and (q.rows, q.cols) != tuple(x.shape)) or \
-            (qt is not None and (qt.cols, qt.rows) != tuple(x.shape)):
-        raise ValueError("q takes x's shape and qt the transposed one")
-    _mx4_call("mgt_mx4_quantize", x.device, stream, (q, qt), code, _ptr(x), ld, _addr(q),
-              _addr(qt))
-
-
-def mx4_dequantize(q, y, stream=None):
-    """y [rows, cols] (fp32 or bf16) = what q stands for (see mgt_mx4_dequantize)."""
-    code, ld = _matrix(y, "y")
-    if tuple(y.shape) != (q.rows, q.cols):
-        raise ValueError("y takes q's shape")
-    _mx4_call("mgt_mx4_dequantize", y.device, stream, (q,), _addr(q), code, _ptr(y), ld)
-
-
-def gemm_mx4(A, B, C, status, stream=None):
-    """C [A.rows, B.rows] (fp32 or bf16) = A B^T of two 4-bit operands (see mgt_gemm_mx4);
-    status an int32 device tensor that receives timeout codes."""
-    code, ld = _matrix(C, "C")
-    _check_status(status)
-    if tuple(C.shape) != (A.rows, B.rows) or A.cols != B.cols:
-        raise ValueError("C must be [A.rows, B.rows], and A and B have the same columns")
-    _mx4_call("mgt_gemm_mx4", C.device, stream, (A, B, status), _addr(A), _addr(B), _ptr(C), code,
-              ld, _ptr(status))
-
-
-def gemm_mx4_gated(X, W, a, status, act="silu", u=None, stream=None):
-    """a = Q(act(gate) * up) with [gate | up] = X W^T, one kernel (see mgt_gemm_mx4_gated): W has
-    a.cols gate rows from row 0 and up rows from row a.cols rounded up to 128. u (bf16
-    [X.rows, 2 a.cols], optional) keeps [gate | up] for the backward."""
-    import torch
-    _check_status(status)
-    ldu = 0
-    if u is not None:
-        if u.dtype != torch.bfloat16:
-            raise TypeError("u must be bfloat16")
-        ldu = _matrix(u, "u")[1]
-        if tuple(u.shape) != (X.rows, 2 * a.cols):
-            raise ValueError("u must be [X.rows, 2 * a.cols]")
-    if act not in ACTIVATIONS:
-        raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
-    _mx4_call("mgt_gemm_mx4_gated", a.codes.device, stream, (X, W, u, status), _addr(X), _addr(W),
-              ACTIVATIONS[act], _addr(a), _ptr(u), ldu, _ptr(status))
-
-
-def mx4_gated_bwd(da, u, du=None, dut=None, at=None, act="silu", stream=None):
-    """Gradients of the gated product from da (bf16 [rows, ffn]) and u = [gate | up] (bf16
-    [rows, 2 ffn]), quantised along the rows (du), along the columns (dut), and the product itself
-    transposed (at); see mgt_mx4_gated_bwd for their layouts."""
-    import torch
-    if da.dtype != torch.bfloat16 or u.dtype != torch.bfloat16:
-        raise TypeError("da and u must be bfloat16")
-    ldda, ldu = _matrix(da, "da")[1], _matrix(u, "u")[1]
-    if tuple(u.shape) != (da.shape[0], 2 * da.shape[1]):
-        raise ValueError("u must be [rows, 2 * ffn]")
-    if act not in ACTIVATIONS:
-        raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
-    _mx4_call("mgt_mx4_gated_bwd", da.device, stream, (u, du, dut, at), ACTIVATIONS[act],
-              da.shape[0], da.shape[1], _ptr(da), ldda, _ptr(u), ldu, _addr(du), _addr(dut),
-              _addr(at))
 
 
 def layernorm_bwd_noalloc(dtype, rows, h, dy, dres, x, gamma, mean, rstd, dx, dgamma, dbeta,

@@ -865,8 +865,8 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   a.err = g.err;
 
   auto kern = mx4_skinny_kernel<FMT, GATED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       227 * 1024);
+  static SmemLimit limit;
+  cudaError_t e = limit.allow(kern, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((g.N + kPRows - 1) / kPRows) * split),
@@ -921,7 +921,8 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
     a.width = store_width(g.C, g.ldc, g.c_f32 ? 4 : 2);
   a.err = g.err;
   auto kern = mx4_pair_kernel<FMT, GATED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.allow(kern, C::kSmem);
   if (e != cudaSuccess) return e;
   const int tiles = a.num_m * a.num_n;
   const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;

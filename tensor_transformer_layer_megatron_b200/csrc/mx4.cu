@@ -501,8 +501,8 @@ cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* 
   const __nv_bfloat16* ub = (const __nv_bfloat16*)u;
   auto k = fmt == kMxfp4 ? mx4_gated_bwd_kernel<kMxfp4> : mx4_gated_bwd_kernel<kNvfp4>;
   constexpr int smem = 3 * kTR * kTC * 4;
-  // Set on every call: the attribute belongs to the current device's copy of the kernel.
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit[2];
+  cudaError_t e = limit[fmt].allow(k, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(tile_grid(rows, F));
   return launch_kernel(true, k, grid, dim3(256), (size_t)smem, s, rows, F, act,

@@ -43,14 +43,22 @@ const float* factor_of(const mgt_mx4* q) {
   return q && q->format == MGT_NVFP4 ? q->factor : nullptr;
 }
 
-// SMs of the current device; 0 where it is not a Blackwell part, -1 on an error.
+// SMs of the current device; 0 where it is not a Blackwell part, -1 on an error. Asked once per
+// device (the answer cannot change).
 int sms() {
+  static std::atomic<int> known[64];  // SMs + 1
   int dev = 0, nsm = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev < 64) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k) return k - 1;
+  }
+  if (cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
     return -1;
-  return major == 10 ? nsm : 0;
+  if (major != 10) nsm = 0;
+  if (dev < 64) known[dev].store(nsm + 1, std::memory_order_relaxed);
+  return nsm;
 }
 #define MX4_SMS(n)             \
   const int n = sms();         \

@@ -3,7 +3,26 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mgt {
+
+// Allow `kern` on the current device `bytes` of dynamic shared memory, once per device (the
+// attribute belongs to a device's copy of the kernel). One object per kernel.
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};
+  template <typename K>
+  cudaError_t allow(K kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // A 4-bit operand: packed codes (rows of ld / 2 bytes), scale tiles, leading dimension.
 struct Mx4Out {

@@ -1,0 +1,212 @@
+"""Microscaled 4-bit operands and operators: the binding of mgt_mx4_* and mgt_gemm_mx4* in
+include/mgt_layer.h. Argument checks and marshalling only; the work is in the CUDA kernels."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, load_library
+
+
+class _Mx4Operand(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+            ("ld", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+            ("factor", ctypes.c_void_p)]
+
+
+MX4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _up128(n):
+    return (n + 127) // 128 * 128
+
+
+class Mx4:
+    """A microscaled 4-bit operand of `rows` by `cols` (see mgt_mx4 in include/mgt_layer.h):
+    device buffers for its codes [rows, ld / 2] and scale tiles, both uint8, and for "nvfp4" its
+    factor {amax, f}, two fp32 on the device. Buffers are allocated (f = 1), or given: codes
+    with rows of ld / 2 contiguous bytes, `scales` with room for whole tiles of 128 rows."""
+
+    def __init__(self, fmt, rows, cols, device="cuda", codes=None, scales=None, factor=None):
+        if fmt not in MX4_FORMATS:
+            raise ValueError("format must be one of %s" % sorted(MX4_FORMATS))
+        rows, cols = int(rows), int(cols)
+        if rows < 1 or cols < 1:
+            raise ValueError("an operand has at least one row and one column")
+        block = 32 if fmt == "mxfp4" else 16
+        if codes is None:
+            codes = torch.empty(rows, _up128(cols) // 2, dtype=torch.uint8, device=device)
+        if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.shape[0] < rows or \
+            codes.stride(1) != 1 or (codes.shape[0] > 1 and
+                                     codes.stride(0) != codes.shape[1]):
+            raise TypeError("codes must be contiguous uint8 [rows, ld / 2]")
+        self.ld = 2 * codes.shape[1]
+        if self.ld % 128 or self.ld < _up128(cols):
+            raise ValueError("ld must be a multiple of 128 that holds all columns")
+        need = _up128(rows) * self.ld // block
+        if scales is None:
+            scales = torch.empty(need, dtype=torch.uint8, device=codes.device)
+        if scales.dtype != torch.uint8 or not scales.is_contiguous():
+            raise TypeError("scales must be contiguous uint8")
+        if scales.numel() < need:
+            raise ValueError("scales need %d bytes" % need)
+        if fmt == "nvfp4" and factor is None:
+            factor = torch.ones(2, dtype=torch.float32, device=codes.device)
+        if factor is not None and (factor.dtype != torch.float32 or factor.numel() < 2 or
+                               not factor.is_contiguous()):
+            raise TypeError("factor must be two contiguous float32")
+        for t in (scales, factor):
+            if t is not None and t.device != codes.device:
+                  raise ValueError("codes, scales and factor must be on one device")
+        self.fmt, self.rows, self.cols = fmt, rows, cols
+        self.codes, self.scales, self.factor, self.device = codes, scales, factor, codes.device
+        self._bind(0, 0)
+
+    def _bind(self, row, col):
+        block = 32 if self.fmt == "mxfp4" else 16
+        self._row, self._col = row, col
+        self._c = _Mx4Operand(
+            MX4_FORMATS[self.fmt], self.rows, self.cols, self.ld,
+            self.codes.data_ptr() + (row * self.ld + col) // 2,
+            self.scales.data_ptr() + 512 * (row // 128 * (self.ld // (4 * block)) +
+                                        col // (4 * block)),
+            None if self.factor is None else self.factor.data_ptr())
+        self._addr = ctypes.addressof(self._c)
+
+    def part(self, row, rows, col, cols):
+        """The operand of rows row .. row + rows - 1 and columns col .. col + cols - 1 of this
+        one, in the same buffers; row and col are multiples of 128."""
+        if row % 128 or col % 128 or row < 0 or col < 0 or rows < 1 or cols < 1 or \
+            row + rows > self.rows or _up128(col + cols) > _up128(self.cols):
+            raise ValueError("a part starts at multiples of 128 and lies inside the operand")
+        p = object.__new__(Mx4)
+        p.fmt, p.rows, p.cols, p.ld = self.fmt, int(rows), int(cols), self.ld
+        p.codes, p.scales, p.factor = self.codes, self.scales, self.factor
+        p.device = self.device
+        p._bind(self._row + row, self._col + col)
+        return p
+
+    def rows_view(self, row, rows):
+        """The operand of rows row .. row + rows - 1 (row a multiple of 128), all columns."""
+        return self.part(row, rows, 0, self.cols)
+
+
+def _matrix(t, name):
+    """(dtype code, row stride) of a 2-D fp32 or bf16 tensor with contiguous rows."""
+    dtype = t.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("%s must be float32 or bfloat16" % name)
+    if t.dim() != 2:
+        raise TypeError("%s must be 2-D with contiguous rows" % name)
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise TypeError("%s must be 2-D with contiguous rows" % name)
+    return (1 if dtype is torch.bfloat16 else 0), (ld if rows > 1 else max(ld, cols))
+
+
+def _call(name, device, stream, others, *args):
+    """Launch on `device` (all tensors' device), on its current stream unless one is given."""
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on one device")
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    else:
+        handle = stream.cuda_stream
+    f = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        code = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, handle)
+    if code:
+        _check(code, name)
+
+
+def _check_status(status):
+    if status.dtype is not torch.int32:
+        raise TypeError("status must be an int32 device word")
+
+
+def _addr(q):
+    return None if q is None else q._addr
+
+
+def mx4_tensor_factor(x, factor, stream=None):
+    """factor = {amax, f} of a 2-D tensor for "nvfp4" (see mgt_mx4_tensor_factor)."""
+    code, ld = _matrix(x, "x")
+    if factor.dtype != torch.float32 or factor.numel() < 2 or not factor.is_contiguous():
+        raise TypeError("factor must be two contiguous float32")
+    _call("mgt_mx4_tensor_factor", x.device, stream, (factor,), code, x.shape[0], x.shape[1],
+          x.data_ptr(), ld, factor.data_ptr())
+
+
+def mx4_quantize(x, q=None, qt=None, stream=None):
+    """Quantise x [rows, cols] (fp32 or bf16) into q and / or, transposed, into qt (see
+    mgt_mx4_quantize)."""
+    code, ld = _matrix(x, "x")
+    if (q is not None and (q.rows, q.cols) != tuple(x.shape)) or \
+            (qt is not None and (qt.cols, qt.rows) != tuple(x.shape)):
+        raise ValueError("q takes x's shape and qt the transposed one")
+    _call("mgt_mx4_quantize", x.device, stream, (q, qt), code, x.data_ptr(), ld, _addr(q),
+          _addr(qt))
+
+
+def mx4_dequantize(q, y, stream=None):
+    """y [rows, cols] (fp32 or bf16) = what q stands for (see mgt_mx4_dequantize)."""
+    code, ld = _matrix(y, "y")
+    if tuple(y.shape) != (q.rows, q.cols):
+        raise ValueError("y takes q's shape")
+    _call("mgt_mx4_dequantize", y.device, stream, (q,), _addr(q), code, y.data_ptr(), ld)
+
+
+def gemm_mx4(A, B, C, status, stream=None):
+    """C [A.rows, B.rows] (fp32 or bf16) = A B^T of two 4-bit operands (see mgt_gemm_mx4);
+    status an int32 device tensor that receives timeout codes."""
+    code, ld = _matrix(C, "C")
+    _check_status(status)
+    if tuple(C.shape) != (A.rows, B.rows) or A.cols != B.cols:
+        raise ValueError("C must be [A.rows, B.rows], and A and B have the same columns")
+    _call("mgt_gemm_mx4", C.device, stream, (A, B, status), _addr(A), _addr(B), C.data_ptr(), code,
+          ld, status.data_ptr())
+
+
+def gemm_mx4_gated(X, W, a, status, act="silu", u=None, stream=None):
+    """a = Q(act(gate) * up) with [gate | up] = X W^T, one kernel (see mgt_gemm_mx4_gated): W has
+    a.cols gate rows from row 0 and up rows from row a.cols rounded up to 128. u (bf16
+    [X.rows, 2 a.cols], optional) keeps [gate | up] for the backward."""
+    _check_status(status)
+    ldu = 0
+    if u is not None:
+        if u.dtype != torch.bfloat16:
+            raise TypeError("u must be bfloat16")
+        ldu = _matrix(u, "u")[1]
+        if tuple(u.shape) != (X.rows, 2 * a.cols):
+            raise ValueError("u must be [X.rows, 2 * a.cols]")
+    if act not in ACTIVATIONS:
+        raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
+    _call("mgt_gemm_mx4_gated", a.device, stream, (X, W, u, status), _addr(X), _addr(W),
+          ACTIVATIONS[act], _addr(a), None if u is None else u.data_ptr(), ldu,
+          status.data_ptr())
+
+
+def mx4_gated_bwd(da, u, du=None, dut=None, at=None, act="silu", stream=None):
+    """Gradients of the gated product from da (bf16 [rows, ffn]) and u = [gate | up] (bf16
+    [rows, 2 ffn]), quantised along the rows (du), along the columns (dut), and the product itself
+    transposed (at); see mgt_mx4_gated_bwd for their layouts."""
+    if da.dtype != torch.bfloat16 or u.dtype != torch.bfloat16:
+        raise TypeError("da and u must be bfloat16")
+    ldda, ldu = _matrix(da, "da")[1], _matrix(u, "u")[1]
+    if tuple(u.shape) != (da.shape[0], 2 * da.shape[1]):
+        raise ValueError("u must be [rows, 2 * ffn]")
+    if act not in ACTIVATIONS:
+        raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
+    _call("mgt_mx4_gated_bwd", da.device, stream, (u, du, dut, at), ACTIVATIONS[act],
+          da.shape[0], da.shape[1], da.data_ptr(), ldda, u.data_ptr(), ldu,
+          _addr(du), _addr(dut), _addr(at))

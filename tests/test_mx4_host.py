@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import tensor_transformer_layer_megatron_b200 as mgt
-from tensor_transformer_layer_megatron_b200 import _Mx4Operand
+from tensor_transformer_layer_megatron_b200.mx4 import _Mx4Operand
 
 OK, EINVAL, EUNSUPPORTED = 0, 1, 2
 P = 0x100000  # an address that is never read
