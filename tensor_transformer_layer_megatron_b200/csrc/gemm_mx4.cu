@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(192)
     const int tokens = min(g.bnq, g.M - q0);
     const uint32_t mine = smem_u32(part + lane * 4);
     const int col = p0 + lane * 4;
-    const float inv_f = GATED && FMT == kNvfp4 ? 1.0f / (g.out_factor ? g.out_factor[1] : 1.f) : 1.f;
+    const Mx4Factor of = mx4_factor<FMT>(GATED ? g.out_factor : nullptr);
 #pragma unroll 2
     for (int t = (int)rank * 4 + (warp - 2); t < tokens; t += 4 * (int)csize) {
       float v[NM][4];
@@ -372,15 +372,10 @@ __global__ void __launch_bounds__(192)
         constexpr int B = Mx4Fmt<FMT>::kBlock;
 #pragma unroll
         for (int o = B / 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const Mx4Block q = mx4_block<FMT>(mx, inv_f);
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = mx4_scaled<FMT>(a[i], q, inv_f);
-          w[i + 4] = 0.f;
-        }
+        const Mx4Block q = mx4_block<FMT>(mx, of);
+        const float w[8] = {a[0], a[1], a[2], a[3], 0.f, 0.f, 0.f, 0.f};
         *reinterpret_cast<uint16_t*>(g.a.codes + (row * g.a.ld + col) / 2) =
-            (uint16_t)(e2m1x8(w) & q.mask);
+            (uint16_t)mx4_codes8<FMT>(w, q, of);
         if (col % B == 0)
           g.a.scales[mx4_scale_off<FMT>(row, col / B, g.a.ld)] = (uint8_t)q.byte;
       }
@@ -693,8 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int ew = warp & 3, set = (warp - 2) >> 2;
     uint8_t* my = stg + (warp - 2) * kStoreBytes;
     const float f = (g.a_factor ? g.a_factor[1] : 1.f) * (g.b_factor ? g.b_factor[1] : 1.f);
-    const float inv_f =
-        GATED && FMT == kNvfp4 ? 1.0f / (g.out_factor ? g.out_factor[1] : 1.f) : 1.f;
+    const Mx4Factor of = mx4_factor<FMT>(GATED ? g.out_factor : nullptr);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t overlap0 = mapa_shared(smem_u32(overlap), 0);
     int acc = 0;
@@ -767,14 +761,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             uint32_t mx = 0;
 #pragma unroll
             for (int k = 0; k < B; ++k) mx = max(mx, abs_bits(v[b * B + k]));
-            const Mx4Block q = mx4_block<FMT>(mx, inv_f);
+            const Mx4Block q = mx4_block<FMT>(mx, of);
             bytes |= q.byte << (8 * b);
 #pragma unroll
             for (int k = 0; k < B / 8; ++k) {
               float e[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) e[j] = v[b * B + k * 8 + j];
-              codes[b * (B / 8) + k] = mx4_codes8<FMT>(e, q, inv_f);
+              codes[b * (B / 8) + k] = mx4_codes8<FMT>(e, q, of);
             }
           }
           if (row < g.M) {

@@ -28,6 +28,12 @@ struct Vec8<__nv_bfloat16> {
     a = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  // Largest |x| as fp32 bits: bf16 magnitudes order like their bits, two to a word.
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = max_u16x2(max_u16x2(a.x & k, a.y & k), max_u16x2(a.z & k, a.w & k));
+    return max(m << 16, m & 0xffff0000u);
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -52,6 +58,10 @@ struct Vec8<float> {
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t amax() const {
+    return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
+               max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -78,6 +88,28 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   return m;
 }
 
+// A walk over (row, group of columns) in row-major order, `stride` items a step, with one
+// division at the start.
+struct Walk {
+  long long row, drow;
+  int g, dg, groups;
+  __device__ __forceinline__ Walk(unsigned long long first, unsigned long long stride, int n) {
+    groups = n;
+    row = (long long)(first / (unsigned)n);
+    g = (int)(first - (unsigned long long)row * (unsigned)n);
+    drow = (long long)(stride / (unsigned)n);
+    dg = (int)(stride - (unsigned long long)drow * (unsigned)n);
+  }
+  __device__ __forceinline__ void step() {
+    row += drow;
+    g += dg;
+    if (g >= groups) {
+      g -= groups;
+      ++row;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------- tensor factor
 // out = {amax over the finite elements, f = 2^ceil(log2(amax / 2688)), 1 for amax = 0}: 2688 =
 // 6 * 448 is the largest product of an element and a block scale. Block maxima meet in an
@@ -87,19 +119,30 @@ template <typename T>
 __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, const T* __restrict__ x,
                                                          long long ldx, bool vec, float* out) {
   __shared__ uint32_t red[8];
-  const uint32_t groups = (uint32_t)(cols + 7) / 8;
-  const unsigned long long n = (unsigned long long)rows * groups;
   uint32_t m = 0;
-  for (unsigned long long i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) {
-    const uint32_t r = (uint32_t)(i / groups), g = (uint32_t)(i - (unsigned long long)r * groups);
-    Vec8<T> w;
-    load8(w, x + (long long)r * ldx, (int)g * 8, cols, true, vec);
-    float v[8];
-    w.get(v);
+  constexpr int U = 4;
+  Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, (cols + 7) / 8);
+  while (at.row < rows) {
+    Vec8<T> w[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t b = abs_bits(v[k]);
-      m = max(m, b < 0x7f800000u ? b : 0u);
+    for (int u = 0; u < U; ++u) {
+      load8(w[u], x + at.row * ldx, at.g * 8, cols, at.row < rows, vec);
+      at.step();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t all = w[u].amax();
+      if (all < 0x7f800000u) {
+        m = max(m, all);
+      } else {  // infinities and NaNs do not count
+        float v[8];
+        w[u].get(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t b = abs_bits(v[k]);
+          m = max(m, b < 0x7f800000u ? b : 0u);
+        }
+      }
     }
   }
   m = __reduce_max_sync(0xffffffffu, m);
@@ -122,6 +165,29 @@ __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, con
   }
 }
 
+// Eight elements of a row (v: their values, m: the largest magnitude's bits) into the row-wise
+// operand; a block's lanes are neighbours: 4 (mxfp4) or 2 (nvfp4).
+template <int FMT>
+__device__ __forceinline__ void store_row8(const float (&v)[8], uint32_t m, const Mx4Out& o,
+                                           long long row, int col, bool ok, const Mx4Factor& f) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const Mx4Block q = mx4_block<FMT>(m, f);
+  const uint32_t codes = mx4_codes8<FMT>(v, q, f);
+  if (ok) {
+    *reinterpret_cast<uint32_t*>(o.codes + (row * o.ld + col) / 2) = codes;
+    if (col % Mx4Fmt<FMT>::kBlock == 0)
+      o.scales[mx4_scale_off<FMT>(row, col / Mx4Fmt<FMT>::kBlock, o.ld)] = (uint8_t)q.byte;
+  }
+}
+template <int FMT, typename T>
+__device__ __forceinline__ void store_row8(const Vec8<T>& w, const Mx4Out& o, long long row,
+                                           int col, bool ok, const Mx4Factor& f) {
+  float v[8];
+  w.get(v);
+  store_row8<FMT>(v, w.amax(), o, row, col, ok, f);
+}
+
 // ---------------------------------------------------------------------------- rows only
 // A warp takes 256 columns of a row, a lane eight of them (16 bytes of bf16); a block's maximum
 // is a shuffle over 4 (mxfp4) or 2 (nvfp4) lanes. Four such items are loaded before the first
@@ -134,37 +200,21 @@ __global__ void __launch_bounds__(256)
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int kp = (cols + 127) & ~127;
-  const uint32_t groups = (uint32_t)(kp + 255) / 256;
-  const unsigned long long n = (unsigned long long)rows * groups;
-  const unsigned long long warps = gridDim.x * 8ull;
-  const float inv_f = FMT == kNvfp4 ? 1.0f / factor[1] : 1.f;
-  for (unsigned long long it = blockIdx.x * 8ull + (threadIdx.x >> 5); it < n; it += U * warps) {
+  const Mx4Factor f = mx4_factor<FMT>(factor);
+  Walk at(blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull, (kp + 255) / 256);
+  while (at.row < rows) {
     Vec8<T> w[U];
-    uint32_t row[U];
+    long long row[U];
     int col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const unsigned long long i = it + u * warps;
-      row[u] = (uint32_t)(i / groups);
-      col[u] = (int)(i - (unsigned long long)row[u] * groups) * 256 + lane * 8;
-      load8(w[u], x + (long long)row[u] * ldx, col[u], cols, i < n, vec);
+      row[u] = at.row;
+      col[u] = at.g * 256 + lane * 8;
+      load8(w[u], x + row[u] * ldx, col[u], cols, row[u] < rows, vec);
+      at.step();
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[8];
-      w[u].get(v);
-      uint32_t m = amax8(v);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const Mx4Block q = mx4_block<FMT>(m, inv_f);
-      const uint32_t codes = mx4_codes8<FMT>(v, q, inv_f);
-      if (it + u * warps < n && col[u] < kp) {
-        *reinterpret_cast<uint32_t*>(out.codes + (row[u] * out.ld + col[u]) / 2) = codes;
-        if (col[u] % Mx4Fmt<FMT>::kBlock == 0)
-          out.scales[mx4_scale_off<FMT>(row[u], col[u] / Mx4Fmt<FMT>::kBlock, out.ld)] =
-              (uint8_t)q.byte;
-      }
-    }
+    for (int u = 0; u < U; ++u) store_row8<FMT>(w[u], out, row[u], col[u], row[u] < rows && col[u] < kp, f);
   }
 }
 
@@ -176,40 +226,23 @@ __global__ void __launch_bounds__(256)
 // sector.
 constexpr int kTR = 64, kTC = 128;
 
-// One matrix: row-wise operand (codes null: none) and transposed operand (codes_t null: none).
-template <int FMT>
-__device__ __forceinline__ void store_row8(const float (&v)[8], const Mx4Out& o, long long row,
-                                           int col, bool ok, float inv_f) {
-  uint32_t m = amax8(v);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const Mx4Block q = mx4_block<FMT>(m, inv_f);
-  const uint32_t codes = mx4_codes8<FMT>(v, q, inv_f);
-  if (ok) {
-    *reinterpret_cast<uint32_t*>(o.codes + (row * o.ld + col) / 2) = codes;
-    if (col % Mx4Fmt<FMT>::kBlock == 0)
-      o.scales[mx4_scale_off<FMT>(row, col / Mx4Fmt<FMT>::kBlock, o.ld)] = (uint8_t)q.byte;
-  }
-}
-
 // Columns c, c + 1 (rows r .. r + 15, values in v[column][row]) into the transposed operand.
 template <int FMT>
 __device__ __forceinline__ void store_col16(float (&v)[2][16], const Mx4Out& o, long long r, int c,
-                                            int cols, float inv_f) {
+                                            int cols, const uint32_t (&amax)[2],
+                                            const Mx4Factor& f) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[k][i]));
+    uint32_t m = amax[k];
     if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    const Mx4Block q = mx4_block<FMT>(m, inv_f);
+    const Mx4Block q = mx4_block<FMT>(m, f);
     float a[8], b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       a[i] = v[k][i];
       b[i] = v[k][8 + i];
     }
-    const uint2 w = make_uint2(mx4_codes8<FMT>(a, q, inv_f), mx4_codes8<FMT>(b, q, inv_f));
+    const uint2 w = make_uint2(mx4_codes8<FMT>(a, q, f), mx4_codes8<FMT>(b, q, f));
     if (c + k < cols) {
       *reinterpret_cast<uint2*>(o.codes + ((long long)(c + k) * o.ld + r) / 2) = w;
       if (r % Mx4Fmt<FMT>::kBlock == 0)
@@ -233,7 +266,10 @@ __device__ __forceinline__ void tile_put(uint8_t* s, int r, int c8, const Vec8<T
   }
 }
 template <typename T>
-__device__ __forceinline__ void tile_get16(const uint8_t* s, int r, int cp, float (&v)[2][16]) {
+__device__ __forceinline__ void tile_get16(const uint8_t* s, int r, int cp, float (&v)[2][16],
+                                           uint32_t (&amax)[2]) {
+  uint32_t m = 0;
+  amax[0] = amax[1] = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if constexpr (sizeof(T) == 2) {
@@ -241,11 +277,18 @@ __device__ __forceinline__ void tile_get16(const uint8_t* s, int r, int cp, floa
           *reinterpret_cast<const uint32_t*>(s + ((r + i) * 64 + (cp ^ (r & 16))) * 4);
       v[0][i] = bf16_lo(w);
       v[1][i] = bf16_hi(w);
+      m = max_u16x2(m, w & 0x7fff7fffu);
     } else {
       const float2 w = *reinterpret_cast<const float2*>(s + ((r + i) * 128 + 2 * cp) * 4);
       v[0][i] = w.x;
       v[1][i] = w.y;
+      amax[0] = max(amax[0], abs_bits(w.x));
+      amax[1] = max(amax[1], abs_bits(w.y));
     }
+  }
+  if constexpr (sizeof(T) == 2) {
+    amax[0] = m << 16;
+    amax[1] = m & 0xffff0000u;
   }
 }
 
@@ -259,7 +302,7 @@ __global__ void __launch_bounds__(256)
   const int tiles_c = (cols + kTC - 1) / kTC;
   const int c0 = (int)(blockIdx.x % tiles_c) * kTC;
   const long long r0 = (long long)(blockIdx.x / tiles_c) * kTR;
-  const float inv_f = FMT == kNvfp4 ? 1.0f / factor[1] : 1.f;
+  const Mx4Factor f = mx4_factor<FMT>(factor);
   const int c8 = threadIdx.x & 15, rr = threadIdx.x >> 4;
   Vec8<T> w[4];
 #pragma unroll
@@ -271,18 +314,15 @@ __global__ void __launch_bounds__(256)
   for (int k = 0; k < 4; ++k) {
     const long long row = r0 + k * 16 + rr;
     tile_put(tile, k * 16 + rr, c8, w[k]);
-    if (out.codes) {
-      float v[8];
-      w[k].get(v);
-      store_row8<FMT>(v, out, row, c0 + c8 * 8, row < rows, inv_f);
-    }
+    if (out.codes) store_row8<FMT>(w[k], out, row, c0 + c8 * 8, row < rows, f);
   }
   __syncthreads();
   const int cp = (warp & 3) * 16 + (lane & 15);
   const int r = (warp >> 2) * 32 + (lane >> 4) * 16;
   float v[2][16];
-  tile_get16<T>(tile, r, cp, v);
-  store_col16<FMT>(v, out_t, r0 + r, c0 + 2 * cp, cols, inv_f);
+  uint32_t m[2];
+  tile_get16<T>(tile, r, cp, v, m);
+  store_col16<FMT>(v, out_t, r0 + r, c0 + 2 * cp, cols, m, f);
 }
 
 // ---------------------------------------------------------------------------- gated backward
@@ -303,10 +343,9 @@ __global__ void __launch_bounds__(256)
   const int tiles_c = (F + kTC - 1) / kTC;
   const int c0 = (int)(blockIdx.x % tiles_c) * kTC;
   const long long r0 = (long long)(blockIdx.x / tiles_c) * kTR;
-  const bool nv = FMT == kNvfp4;
-  const float if_du = nv && dg.codes ? 1.0f / f_du[1] : 1.f;
-  const float if_dut = nv && dgt.codes ? 1.0f / f_dut[1] : 1.f;
-  const float if_at = nv && at.codes ? 1.0f / f_at[1] : 1.f;
+  const Mx4Factor if_du = mx4_factor<FMT>(dg.codes ? f_du : nullptr);
+  const Mx4Factor if_dut = mx4_factor<FMT>(dgt.codes ? f_dut : nullptr);
+  const Mx4Factor if_at = mx4_factor<FMT>(at.codes ? f_at : nullptr);
   const int c8 = threadIdx.x & 15, rr = threadIdx.x >> 4;
   const int col = c0 + c8 * 8;
   Vec8<__nv_bfloat16> wd[4], wg[4], wu[4];
@@ -343,23 +382,24 @@ __global__ void __launch_bounds__(256)
     s[0] = make_float4(a[0], a[1], a[2], a[3]);
     s[1] = make_float4(a[4], a[5], a[6], a[7]);
     if (dg.codes) {
-      store_row8<FMT>(g, dg, row, col, row < rows, if_du);
-      store_row8<FMT>(p, dup, row, col, row < rows, if_du);
+      store_row8<FMT>(g, amax8(g), dg, row, col, row < rows, if_du);
+      store_row8<FMT>(p, amax8(p), dup, row, col, row < rows, if_du);
     }
   }
   __syncthreads();
   const int cp = (warp & 3) * 16 + (lane & 15);
   const int r = (warp >> 2) * 32 + (lane >> 4) * 16;
   float v[2][16];
+  uint32_t m[2];
   if (dgt.codes) {
-    tile_get16<float>(tiles, r, cp, v);
-    store_col16<FMT>(v, dgt, r0 + r, c0 + 2 * cp, F, if_dut);
-    tile_get16<float>(tiles + kTile, r, cp, v);
-    store_col16<FMT>(v, dupt, r0 + r, c0 + 2 * cp, F, if_dut);
+    tile_get16<float>(tiles, r, cp, v, m);
+    store_col16<FMT>(v, dgt, r0 + r, c0 + 2 * cp, F, m, if_dut);
+    tile_get16<float>(tiles + kTile, r, cp, v, m);
+    store_col16<FMT>(v, dupt, r0 + r, c0 + 2 * cp, F, m, if_dut);
   }
   if (at.codes) {
-    tile_get16<float>(tiles + 2 * kTile, r, cp, v);
-    store_col16<FMT>(v, at, r0 + r, c0 + 2 * cp, F, if_at);
+    tile_get16<float>(tiles + 2 * kTile, r, cp, v, m);
+    store_col16<FMT>(v, at, r0 + r, c0 + 2 * cp, F, m, if_at);
   }
 }
 
@@ -371,12 +411,11 @@ __global__ void __launch_bounds__(256)
                           const float* __restrict__ factor, T* __restrict__ y, long long ldy,
                           bool vec) {
   grid_dependency_wait();
-  const uint32_t groups = (uint32_t)(cols + 7) / 8;
-  const unsigned long long n = (unsigned long long)rows * groups;
   const float f = FMT == kNvfp4 ? factor[1] : 1.f;
-  for (unsigned long long i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) {
-    const uint32_t r = (uint32_t)(i / groups);
-    const int c = (int)(i - (unsigned long long)r * groups) * 8;
+  for (Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, (cols + 7) / 8);
+       at.row < rows; at.step()) {
+    const long long r = at.row;
+    const int c = at.g * 8;
     const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + (r * ld + c) / 2));
     const float s =
         mx4_scale_value<FMT>(__ldg(scales + mx4_scale_off<FMT>(r, c / Mx4Fmt<FMT>::kBlock, ld))) *
@@ -390,7 +429,7 @@ __global__ void __launch_bounds__(256)
                               : __uint_as_float((((mag >> 1) + 126u) << 23) | ((mag & 1u) << 22));
       v[k] = (c4 & 8u ? -a : a) * s;
     }
-    T* o = y + (long long)r * ldy + c;
+    T* o = y + r * ldy + c;
     if (vec && c + 8 <= cols) {
       if constexpr (sizeof(T) == 2) {
         uint4 p;

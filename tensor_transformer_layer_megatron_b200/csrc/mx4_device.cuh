@@ -36,53 +36,94 @@ __device__ __forceinline__ long long mx4_scale_off(long long r, int b, long long
          4 * ((r >> 5) & 3) + (b & 3);
 }
 
+// The fp32 value of a scale byte (without the tensor's factor).
+template <int FMT>
+__device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
+  if constexpr (FMT == kMxfp4) {
+    if (byte == 255u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(byte ? byte << 23 : 0x00400000u);  // 2^-127 is subnormal
+  } else {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)byte));
+    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+  }
+}
+
+// Tensor factor as the quantisers use it.
+struct Mx4Factor {
+  float f, inv;
+  bool tiny;  // f below 2^-100: f s could be subnormal
+};
+template <int FMT>
+__device__ __forceinline__ Mx4Factor mx4_factor(const float* factor) {
+  Mx4Factor t = {1.f, 1.f, false};
+  if (FMT == kNvfp4 && factor) {
+    t.f = factor[1];
+    t.inv = 1.0f / t.f;
+    t.tiny = t.f < 7.8886091e-31f;
+  }
+  return t;
+}
+
 // What a block's elements are multiplied by, and the byte that stands for its scale.
 struct Mx4Block {
-  float inv;      // mxfp4: 2^-e. nvfp4: 1 / s, correctly rounded (0 for a block of zeros)
-  float s;        // nvfp4: s
+  float inv;      // mxfp4: 2^-e. nvfp4: 1 / (f s), within two units in the last place
+  float fs;       // nvfp4: f s
   uint32_t byte;  // mxfp4: e + 127 (255 = NaN). nvfp4: e4m3 (0x7f = NaN)
   uint32_t mask;  // codes are ANDed with it: 0 for a block without a usable scale
+  bool wide;      // nvfp4: x / (f s) may leave fp32's range
 };
 
 // From the largest |x| of the block as fp32 bits (NaN above infinity above every number). A
 // block that holds an infinity or a NaN gets the scale NaN and zero codes.
 template <int FMT>
-__device__ __forceinline__ Mx4Block mx4_block(uint32_t amax_bits, float inv_f) {
+__device__ __forceinline__ Mx4Block mx4_block(uint32_t amax_bits, const Mx4Factor& f) {
   Mx4Block q;
   if constexpr (FMT == kMxfp4) {
     const int eb = (int)(amax_bits >> 23);  // floor(log2 amax) + 127; 0 for subnormals
-    q.byte = eb == 255 ? 255u : (uint32_t)max(eb - 2, 0);
-    q.inv = __uint_as_float((254u - q.byte) << 23);
-    q.s = 0.f;
-    q.mask = eb == 255 ? 0u : 0xffffffffu;
-    if (eb == 255) q.inv = 0.f;
+    const bool bad = eb == 255;
+    q.byte = bad ? 255u : (uint32_t)max(eb - 2, 0);
+    q.inv = bad ? 0.f : __uint_as_float((254u - q.byte) << 23);
+    q.mask = bad ? 0u : 0xffffffffu;
+    q.fs = 0.f;
+    q.wide = false;
   } else {
-    const float t = fminf(__uint_as_float(amax_bits) * inv_f, 3.4028234e38f) / 6.0f;
+    // t = amax / (6 f): the quotient by 6 from its rounded reciprocal and one residual, correctly
+    // rounded (see mx4_scaled)
+    constexpr float kSixth = 1.0f / 6.0f;
+    const float u = fminf(__uint_as_float(amax_bits) * f.inv, 3.4028234e38f);
+    const float y = u * kSixth;
+    const float t = fmaf(fmaf(-y, 6.0f, u), kSixth, y);
     uint16_t e;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(t));
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(e));
-    q.s = __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+    const float s = __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
     const bool bad = amax_bits >= 0x7f800000u;
     q.byte = bad ? 0x7fu : (uint32_t)(e & 0xffu);
-    q.mask = (bad || q.s == 0.f) ? 0u : 0xffffffffu;
-    q.inv = q.mask ? __frcp_rn(q.s) : 0.f;
+    q.mask = (bad || s == 0.f) ? 0u : 0xffffffffu;
+    q.fs = f.f * s;
+    q.inv = q.mask ? f.inv * rcp_approx(s) : 0.f;
+    q.wide = f.tiny || t > 896.0f;
   }
   return q;
 }
 
-// The scaled element. nvfp4: (x / f) / s by a product with the rounded reciprocal and one
-// residual correction, which gives the correctly rounded quotient (P. Markstein, Computation of
-// elementary functions on the IBM RISC System/6000 processor, 1990: theorem 1).
+// The scaled element. nvfp4: x / (f s) by a product with the reciprocal and one residual
+// correction (P. Markstein, Computation of elementary functions on the IBM RISC System/6000
+// processor, 1990): the residual is exact, so the value that the last step rounds is within
+// 2^-45 of the quotient, which is far less than an unequal quotient's distance from a border.
 template <int FMT>
-__device__ __forceinline__ float mx4_scaled(float x, const Mx4Block& q, float inv_f) {
-  if constexpr (FMT == kMxfp4) {
-    return x * q.inv;
-  } else {
-    const float xs = fmaxf(fminf(x * inv_f, 3.4028234e38f), -3.4028234e38f);
-    const float y = xs * q.inv;
-    return fmaf(fmaf(-y, q.s, xs), q.inv, y);
-  }
+__device__ __forceinline__ float mx4_scaled(float x, const Mx4Block& q) {
+  const float y = x * q.inv;
+  if constexpr (FMT == kMxfp4) return y;
+  return fmaf(fmaf(-y, q.fs, x), q.inv, y);
+}
+// The same for a block whose quotients may overflow (a kept factor far too small: they saturate)
+// or whose f s may be subnormal: first x / f, clamped to fp32's range, then by s.
+__device__ __forceinline__ float mx4_scaled_wide(float x, uint32_t byte, float inv_f) {
+  return fmaxf(fminf(x * inv_f, 3.4028234e38f), -3.4028234e38f) /
+         mx4_scale_value<kNvfp4>(byte);
 }
 
 // Eight fp32 values to eight e2m1 codes (round to nearest, ties to even, saturating at 6), the
@@ -102,26 +143,23 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
 
 template <int FMT>
 __device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], const Mx4Block& q,
-                                               float inv_f) {
+                                               const Mx4Factor& f) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = mx4_scaled<FMT>(x[i], q, inv_f);
+  for (int i = 0; i < 8; ++i) v[i] = mx4_scaled<FMT>(x[i], q);
+  if (FMT == kNvfp4 && q.wide) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = mx4_scaled_wide(x[i], q.byte, f.inv);
+  }
   return e2m1x8(v) & q.mask;
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// The fp32 value of a scale byte (without the tensor's factor).
-template <int FMT>
-__device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
-  if constexpr (FMT == kMxfp4) {
-    if (byte == 255u) return __uint_as_float(0x7fc00000u);
-    return __uint_as_float(byte ? byte << 23 : 0x00400000u);  // 2^-127 is subnormal
-  } else {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)byte));
-    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
-  }
+// Larger of two pairs of 16-bit values.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Activation of a gated block and its derivative. act: 0 silu, 1 gelu (erf), 2 gelu (tanh). A
@@ -130,7 +168,8 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
 // negative tail, where 1 + erf and 1 + tanh cancel.
 __device__ __forceinline__ void gate_and_grad(float z, int act, float& h, float& dh) {
   if (act == 0) {
-    silu_and_grad_f(z, h, dh);
+    // e^-z and the reciprocal from the special-function unit (relative error about 2^-21 + |z| 2^-24)
+    silu_and_grad_bf16out(z, h, dh);
   } else if (act == 1) {
     const float c = 0.5f * erfcf(z * -0.7071067811865476f);
     h = z * c;
