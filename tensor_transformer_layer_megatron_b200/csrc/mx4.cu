@@ -28,6 +28,10 @@ struct Vec8<__nv_bfloat16> {
     a = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float at(int j) const {
+    const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
+    return j & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
   // Largest |x| as fp32 bits: bf16 magnitudes order like their bits, two to a word.
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t k = 0x7fff7fffu;
@@ -58,6 +62,10 @@ struct Vec8<float> {
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float at(int j) const {
+    return j < 4 ? (j < 2 ? (j ? a.y : a.x) : (j == 2 ? a.z : a.w))
+                 : (j < 6 ? (j == 4 ? b.x : b.y) : (j == 6 ? b.z : b.w));
+  }
   __device__ __forceinline__ uint32_t amax() const {
     return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
                max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
@@ -79,13 +87,6 @@ __device__ __forceinline__ void load8(Vec8<T>& r, const T* row, int c, int cols,
     r.load(row + c);
   else
     r.load_n(row + c, cols - c);
-}
-
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-  return m;
 }
 
 // A walk over (row, group of columns) in row-major order, `stride` items a step, with one
@@ -165,291 +166,279 @@ __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, con
   }
 }
 
-// Eight elements of a row (v: their values, m: the largest magnitude's bits) into the row-wise
-// operand; a block's lanes are neighbours: 4 (mxfp4) or 2 (nvfp4).
-template <int FMT>
-__device__ __forceinline__ void store_row8(const float (&v)[8], uint32_t m, const Mx4Out& o,
-                                           long long row, int col, bool ok, const Mx4Factor& f) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const Mx4Block q = mx4_block<FMT>(m, f);
-  const uint32_t codes = mx4_codes8<FMT>(v, q, f);
-  if (ok) {
-    *reinterpret_cast<uint32_t*>(o.codes + (row * o.ld + col) / 2) = codes;
-    if (col % Mx4Fmt<FMT>::kBlock == 0)
-      o.scales[mx4_scale_off<FMT>(row, col / Mx4Fmt<FMT>::kBlock, o.ld)] = (uint8_t)q.byte;
-  }
-}
-template <int FMT, typename T>
-__device__ __forceinline__ void store_row8(const Vec8<T>& w, const Mx4Out& o, long long row,
-                                           int col, bool ok, const Mx4Factor& f) {
-  float v[8];
-  w.get(v);
-  store_row8<FMT>(v, w.amax(), o, row, col, ok, f);
-}
-
-// ---------------------------------------------------------------------------- rows only
-// A warp takes 256 columns of a row, a lane eight of them (16 bytes of bf16); a block's maximum
-// is a shuffle over 4 (mxfp4) or 2 (nvfp4) lanes. Four such items are loaded before the first
-// is used, so a full grid keeps 64 KB of bf16 in flight per SM.
-template <int FMT, typename T>
-__global__ void __launch_bounds__(256)
-    mx4_rows_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
-                    const float* __restrict__ factor, Mx4Out out) {
-  constexpr int U = 4;
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int kp = (cols + 127) & ~127;
-  const Mx4Factor f = mx4_factor<FMT>(factor);
-  Walk at(blockIdx.x * 8ull + (threadIdx.x >> 5), gridDim.x * 8ull, (kp + 255) / 256);
-  while (at.row < rows) {
-    Vec8<T> w[U];
-    long long row[U];
-    int col[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      row[u] = at.row;
-      col[u] = at.g * 256 + lane * 8;
-      load8(w[u], x + row[u] * ldx, col[u], cols, row[u] < rows, vec);
-      at.step();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) store_row8<FMT>(w[u], out, row[u], col[u], row[u] < rows && col[u] < kp, f);
-  }
-}
-
 // ---------------------------------------------------------------------------- rows and columns
-// A CTA takes 64 rows by 128 columns. Sixteen threads hold a row (eight columns each): they
-// quantise along the row from registers and put the values into shared memory, from where a
-// thread takes 16 rows of two neighbouring columns and quantises along the column; for mxfp4 two
-// lanes 16 apart share a block of 32 rows. 64 rows are 32 bytes of a transposed row: one whole
-// sector.
-constexpr int kTR = 64, kTC = 128;
+// A lane holds a patch of 8 rows by PC columns, a warp 4 x 8 patches (32 rows by 8 PC columns), a
+// CTA four warps below one another (128 rows). A patch gives whole 32-bit words of codes along its
+// rows and along its columns, and the largest magnitude of a block is a shuffle over the two or
+// four (gated: four or eight) lanes that share it, along either direction: the transposed operand
+// needs no trip through shared memory, and a lane has eight loads in flight.
+constexpr int kTileRows = 128;
+constexpr int kTileThreads = 128;
 
-// Columns c, c + 1 (rows r .. r + 15, values in v[column][row]) into the transposed operand.
-template <int FMT>
-__device__ __forceinline__ void store_col16(float (&v)[2][16], const Mx4Out& o, long long r, int c,
-                                            int cols, const uint32_t (&amax)[2],
-                                            const Mx4Factor& f) {
+struct Patch {
+  long long r;  // first row
+  int c;        // first column
+  template <int PC>
+  __device__ __forceinline__ static Patch of(int cols) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tiles_c = (((cols + 127) & ~127) + 8 * PC - 1) / (8 * PC);
+    const unsigned tr = blockIdx.x / (unsigned)tiles_c, tc = blockIdx.x - tr * (unsigned)tiles_c;
+    return Patch{(long long)tr * kTileRows + warp * 32 + (lane >> 3) * 8,
+                 (int)tc * 8 * PC + (lane & 7) * PC};
+  }
+};
+
+// Largest magnitude over the N lanes, a power of two, that share a block; `step` lanes apart.
+template <int N>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m, int step) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    uint32_t m = amax[k];
-    if (FMT == kMxfp4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    const Mx4Block q = mx4_block<FMT>(m, f);
-    float a[8], b[8];
+  for (int o = 1; o < N; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o * step));
+  return m;
+}
+
+// Codes of PC = 8 or 4 consecutive elements.
+template <int FMT, int PC>
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[PC], const Mx4Block& q,
+                                             const Mx4Factor& f) {
+  if constexpr (PC == 8) {
+    return mx4_codes8<FMT>(v, q, f);
+  } else {
+    const float w[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
+    return mx4_codes8<FMT>(w, q, f);
+  }
+}
+
+// Row-wise operand: row i of the patch, v its PC elements, m their largest magnitude's bits.
+template <int FMT, int PC>
+__device__ __forceinline__ void put_row(const float (&v)[PC], uint32_t m, uint8_t* codes,
+                                        uint8_t* scale, bool ok, bool first, const Mx4Factor& f) {
+  const Mx4Block q = mx4_block<FMT>(lanes_max<Mx4Fmt<FMT>::kBlock / PC>(m, 1), f);
+  const uint32_t w = codes_of<FMT, PC>(v, q, f);
+  if (ok) {
+    if constexpr (PC == 8)
+      *reinterpret_cast<uint32_t*>(codes) = w;
+    else
+      *reinterpret_cast<uint16_t*>(codes) = (uint16_t)w;
+    if (first) *scale = (uint8_t)q.byte;
+  }
+}
+// Transposed operand: column j of the patch, v its eight elements.
+template <int FMT>
+__device__ __forceinline__ void put_col(const float (&v)[8], uint32_t m, uint8_t* codes,
+                                        uint8_t* scale, bool ok, bool first, const Mx4Factor& f) {
+  const Mx4Block q = mx4_block<FMT>(lanes_max<Mx4Fmt<FMT>::kBlock / 8>(m, 8), f);
+  const uint32_t w = mx4_codes8<FMT>(v, q, f);
+  if (ok) {
+    *reinterpret_cast<uint32_t*>(codes) = w;
+    if (first) *scale = (uint8_t)q.byte;
+  }
+}
+
+// Addresses of a patch in one operand: rows (columns) i of the patch follow each other by `ld / 2`
+// bytes of codes and 16 bytes of scales (the eight lie in one group of 32).
+struct PatchOut {
+  uint8_t *codes, *scale;
+  long long step;
+  bool first;  // this lane writes the block's scale
+  template <int FMT>
+  __device__ __forceinline__ static PatchOut of(const Mx4Out& o, long long row, long long col) {
+    return PatchOut{o.codes + (row * o.ld + col) / 2,
+                    o.scales + mx4_scale_off<FMT>(row, (int)(col / Mx4Fmt<FMT>::kBlock), o.ld),
+                    o.ld / 2, col % Mx4Fmt<FMT>::kBlock == 0};
+  }
+};
+
+template <int FMT, typename T, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(kTileThreads)
+    mx4_quantize_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
+                        const float* __restrict__ factor, Mx4Out out, Mx4Out out_t) {
+  grid_dependency_wait();
+  const Patch p = Patch::of<8>(cols);
+  if (!COLS && p.r - (threadIdx.x & 24) >= rows) return;  // the whole warp is behind the last row
+  const int kp = (cols + 127) & ~127;
+  Vec8<T> w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load8(w[i], x + (p.r + i) * ldx, p.c, cols, p.r + i < rows, vec);
+  const Mx4Factor f = mx4_factor<FMT>(factor);
+  if constexpr (ROWS) {
+    const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = v[k][i];
-      b[i] = v[k][8 + i];
-    }
-    const uint2 w = make_uint2(mx4_codes8<FMT>(a, q, f), mx4_codes8<FMT>(b, q, f));
-    if (c + k < cols) {
-      *reinterpret_cast<uint2*>(o.codes + ((long long)(c + k) * o.ld + r) / 2) = w;
-      if (r % Mx4Fmt<FMT>::kBlock == 0)
-        o.scales[mx4_scale_off<FMT>(c + k, (int)(r / Mx4Fmt<FMT>::kBlock), o.ld)] =
-            (uint8_t)q.byte;
+      float v[8];
+      w[i].get(v);
+      put_row<FMT, 8>(v, w[i].amax(), o.codes + i * o.step, o.scale + 16 * i,
+                      p.r + i < rows && p.c < kp, o.first, f);
     }
   }
-}
-
-// Shared-memory tile of one matrix. bf16: words of two columns, the halves of a 64-word row
-// swapped on every other group of 16 rows, so that the two half-warps, 16 rows apart, read
-// different banks. fp32: plain rows (a half-warp reads 128 bytes).
-template <typename T>
-__device__ __forceinline__ void tile_put(uint8_t* s, int r, int c8, const Vec8<T>& w) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(s + (r * 64 + ((c8 * 4) ^ ((r & 16)))) * 4) = w.a;
-  } else {
-    float4* d = reinterpret_cast<float4*>(s + (r * 128 + c8 * 8) * 4);
-    d[0] = w.a;
-    d[1] = w.b;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void tile_get16(const uint8_t* s, int r, int cp, float (&v)[2][16],
-                                           uint32_t (&amax)[2]) {
-  uint32_t m = 0;
-  amax[0] = amax[1] = 0;
+  if constexpr (COLS) {
+    const PatchOut o = PatchOut::of<FMT>(out_t, p.c, p.r);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(s + ((r + i) * 64 + (cp ^ (r & 16))) * 4);
-      v[0][i] = bf16_lo(w);
-      v[1][i] = bf16_hi(w);
-      m = max_u16x2(m, w & 0x7fff7fffu);
-    } else {
-      const float2 w = *reinterpret_cast<const float2*>(s + ((r + i) * 128 + 2 * cp) * 4);
-      v[0][i] = w.x;
-      v[1][i] = w.y;
-      amax[0] = max(amax[0], abs_bits(w.x));
-      amax[1] = max(amax[1], abs_bits(w.y));
+    for (int j = 0; j < 8; ++j) {
+      float v[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = w[i].at(j);
+        m = max(m, abs_bits(v[i]));
+      }
+      put_col<FMT>(v, m, o.codes + j * o.step, o.scale + 16 * j, p.c + j < cols, o.first, f);
     }
   }
-  if constexpr (sizeof(T) == 2) {
-    amax[0] = m << 16;
-    amax[1] = m & 0xffff0000u;
-  }
-}
-
-template <int FMT, typename T>
-__global__ void __launch_bounds__(256)
-    mx4_both_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
-                    const float* __restrict__ factor, Mx4Out out, Mx4Out out_t) {
-  __shared__ __align__(16) uint8_t tile[kTR * kTC * sizeof(T)];
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tiles_c = (cols + kTC - 1) / kTC;
-  const int c0 = (int)(blockIdx.x % tiles_c) * kTC;
-  const long long r0 = (long long)(blockIdx.x / tiles_c) * kTR;
-  const Mx4Factor f = mx4_factor<FMT>(factor);
-  const int c8 = threadIdx.x & 15, rr = threadIdx.x >> 4;
-  Vec8<T> w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long row = r0 + k * 16 + rr;
-    load8(w[k], x + row * ldx, c0 + c8 * 8, cols, row < rows, vec);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long row = r0 + k * 16 + rr;
-    tile_put(tile, k * 16 + rr, c8, w[k]);
-    if (out.codes) store_row8<FMT>(w[k], out, row, c0 + c8 * 8, row < rows, f);
-  }
-  __syncthreads();
-  const int cp = (warp & 3) * 16 + (lane & 15);
-  const int r = (warp >> 2) * 32 + (lane >> 4) * 16;
-  float v[2][16];
-  uint32_t m[2];
-  tile_get16<T>(tile, r, cp, v, m);
-  store_col16<FMT>(v, out_t, r0 + r, c0 + 2 * cp, cols, m, f);
 }
 
 // ---------------------------------------------------------------------------- gated backward
 // From da = dL/da and u = [gate | up]: dg = da * up * act'(gate), dup = da * act(gate), and
 // a = act(gate) * up again. dg and dup leave quantised along the rows (for dX) and along the
-// columns (for dW1), a along the columns (for dW2); none of them is written in 16 bits.
+// columns (for dW1), a along the columns (for dW2); none of them is written in 16 bits. Patches of
+// 8 x 4: three results of 32 values stay in registers.
+struct Quad {  // four consecutive bf16
+  uint2 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int cols, bool row_ok,
+                                       bool vec) {
+    a = make_uint2(0, 0);
+    if (!row_ok || c >= cols) return;
+    if (vec && c + 4 <= cols) {
+      a = __ldg(reinterpret_cast<const uint2*>(row + c));
+    } else {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = c + i < cols ? __bfloat16_as_ushort(row[c + i]) : 0;
+      a = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    const uint32_t w = j < 2 ? a.x : a.y;
+    return j & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+
 template <int FMT>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ void put_patch_rows(const float (&v)[8][4], const Mx4Out& out,
+                                               const Patch& p, int rows, const Mx4Factor& f) {
+  const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = max(max(abs_bits(v[i][0]), abs_bits(v[i][1])),
+                           max(abs_bits(v[i][2]), abs_bits(v[i][3])));
+    put_row<FMT, 4>(v[i], m, o.codes + i * o.step, o.scale + 16 * i, p.r + i < rows, o.first, f);
+  }
+}
+template <int FMT>
+__device__ __forceinline__ void put_patch_cols(const float (&v)[8][4], const Mx4Out& out,
+                                               const Patch& p, int cols, const Mx4Factor& f) {
+  const PatchOut o = PatchOut::of<FMT>(out, p.c, p.r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float c[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = v[i][j];
+      m = max(m, abs_bits(c[i]));
+    }
+    put_col<FMT>(c, m, o.codes + j * o.step, o.scale + 16 * j, p.c + j < cols, o.first, f);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kTileThreads)
     mx4_gated_bwd_kernel(int rows, int F, int act, const __nv_bfloat16* __restrict__ da,
                          long long ldda, bool vec_da, const __nv_bfloat16* __restrict__ u,
                          long long ldu, bool vec_g, bool vec_u, const float* __restrict__ f_du,
                          const float* __restrict__ f_dut, const float* __restrict__ f_at,
                          Mx4Out dg, Mx4Out dup, Mx4Out dgt, Mx4Out dupt, Mx4Out at) {
-  extern __shared__ __align__(16) uint8_t tiles[];
-  constexpr int kTile = kTR * kTC * 4;
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tiles_c = (F + kTC - 1) / kTC;
-  const int c0 = (int)(blockIdx.x % tiles_c) * kTC;
-  const long long r0 = (long long)(blockIdx.x / tiles_c) * kTR;
-  const Mx4Factor if_du = mx4_factor<FMT>(dg.codes ? f_du : nullptr);
-  const Mx4Factor if_dut = mx4_factor<FMT>(dgt.codes ? f_dut : nullptr);
-  const Mx4Factor if_at = mx4_factor<FMT>(at.codes ? f_at : nullptr);
-  const int c8 = threadIdx.x & 15, rr = threadIdx.x >> 4;
-  const int col = c0 + c8 * 8;
-  Vec8<__nv_bfloat16> wd[4], wg[4], wu[4];
+  const Patch p = Patch::of<4>(F);
+  Quad wd[8], wg[8], wu[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long row = r0 + k * 16 + rr;
-    load8(wd[k], da + row * ldda, col, F, row < rows, vec_da);
-    load8(wg[k], u + row * ldu, col, F, row < rows, vec_g);
-    load8(wu[k], u + row * ldu + F, col, F, row < rows, vec_u);
+  for (int i = 0; i < 8; ++i) {
+    const long long row = p.r + i;
+    wd[i].load(da + row * ldda, p.c, F, row < rows, vec_da);
+    wg[i].load(u + row * ldu, p.c, F, row < rows, vec_g);
+    wu[i].load(u + row * ldu + F, p.c, F, row < rows, vec_u);
   }
+  float g[8][4], q[8][4], a[8][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long row = r0 + k * 16 + rr;
-    float d[8], g[8], p[8], a[8];
-    wd[k].get(d);
-    wg[k].get(g);
-    wu[k].get(p);
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < 4; ++j) {
       float h, dh;
-      gate_and_grad(g[i], act, h, dh);
-      a[i] = h * p[i];
-      g[i] = d[i] * p[i] * dh;
-      p[i] = d[i] * h;
+      gate_and_grad(wg[i].at(j), act, h, dh);
+      const float d = wd[i].at(j), up = wu[i].at(j);
+      g[i][j] = d * up * dh;
+      q[i][j] = d * h;
+      a[i][j] = h * up;
     }
-    const int at_row = (k * 16 + rr) * 128 + c8 * 8;
-    float4* s = reinterpret_cast<float4*>(tiles + at_row * 4);
-    s[0] = make_float4(g[0], g[1], g[2], g[3]);
-    s[1] = make_float4(g[4], g[5], g[6], g[7]);
-    s = reinterpret_cast<float4*>(tiles + kTile + at_row * 4);
-    s[0] = make_float4(p[0], p[1], p[2], p[3]);
-    s[1] = make_float4(p[4], p[5], p[6], p[7]);
-    s = reinterpret_cast<float4*>(tiles + 2 * kTile + at_row * 4);
-    s[0] = make_float4(a[0], a[1], a[2], a[3]);
-    s[1] = make_float4(a[4], a[5], a[6], a[7]);
-    if (dg.codes) {
-      store_row8<FMT>(g, amax8(g), dg, row, col, row < rows, if_du);
-      store_row8<FMT>(p, amax8(p), dup, row, col, row < rows, if_du);
-    }
+  if (dg.codes) {
+    const Mx4Factor f = mx4_factor<FMT>(f_du);
+    put_patch_rows<FMT>(g, dg, p, rows, f);
+    put_patch_rows<FMT>(q, dup, p, rows, f);
   }
-  __syncthreads();
-  const int cp = (warp & 3) * 16 + (lane & 15);
-  const int r = (warp >> 2) * 32 + (lane >> 4) * 16;
-  float v[2][16];
-  uint32_t m[2];
   if (dgt.codes) {
-    tile_get16<float>(tiles, r, cp, v, m);
-    store_col16<FMT>(v, dgt, r0 + r, c0 + 2 * cp, F, m, if_dut);
-    tile_get16<float>(tiles + kTile, r, cp, v, m);
-    store_col16<FMT>(v, dupt, r0 + r, c0 + 2 * cp, F, m, if_dut);
+    const Mx4Factor f = mx4_factor<FMT>(f_dut);
+    put_patch_cols<FMT>(g, dgt, p, F, f);
+    put_patch_cols<FMT>(q, dupt, p, F, f);
   }
-  if (at.codes) {
-    tile_get16<float>(tiles + 2 * kTile, r, cp, v, m);
-    store_col16<FMT>(v, at, r0 + r, c0 + 2 * cp, F, m, if_at);
-  }
+  if (at.codes) put_patch_cols<FMT>(a, at, p, F, mx4_factor<FMT>(f_at));
 }
 
 // ---------------------------------------------------------------------------- and back
+// A lane decodes eight columns of eight rows, four rows apart, so that a warp's stores cover 128
+// consecutive bytes (bf16) of four rows.
 template <int FMT, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kTileThreads)
     mx4_dequantize_kernel(int rows, int cols, const uint8_t* __restrict__ codes,
                           const uint8_t* __restrict__ scales, long long ld,
                           const float* __restrict__ factor, T* __restrict__ y, long long ldy,
                           bool vec) {
   grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles_c = (cols + 63) / 64;
+  const unsigned tr = blockIdx.x / (unsigned)tiles_c, tc = blockIdx.x - tr * (unsigned)tiles_c;
+  const long long r0 = (long long)tr * kTileRows + warp * 32;
+  const int c = (int)tc * 64 + (lane & 7) * 8;
+  if (r0 >= rows || c >= cols) return;
   const float f = FMT == kNvfp4 ? factor[1] : 1.f;
-  for (Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, (cols + 7) / 8);
-       at.row < rows; at.step()) {
-    const long long r = at.row;
-    const int c = at.g * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + (r * ld + c) / 2));
-    const float s =
-        mx4_scale_value<FMT>(__ldg(scales + mx4_scale_off<FMT>(r, c / Mx4Fmt<FMT>::kBlock, ld))) *
-        f;
-    float v[8];
+  const int lr = lane >> 3;
+  const uint8_t* cp = codes + ((r0 + lr) * ld + c) / 2;
+  const uint8_t* sp = scales + mx4_scale_off<FMT>(r0 + lr, c / Mx4Fmt<FMT>::kBlock, ld);
+  uint32_t w[8], sb[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // magnitude code: 0, 0.5, then 1.m * 2^(e - 1)
-      const uint32_t c4 = w >> (4 * k), mag = c4 & 7u;
-      const float a = mag < 2 ? 0.5f * mag
-                              : __uint_as_float((((mag >> 1) + 126u) << 23) | ((mag & 1u) << 22));
-      v[k] = (c4 & 8u ? -a : a) * s;
-    }
-    T* o = y + r * ldy + c;
+  for (int i = 0; i < 8; ++i) {
+    const bool ok = r0 + lr + 4 * i < rows;
+    w[i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(cp + i * 2 * ld)) : 0;
+    sb[i] = ok ? __ldg(sp + 64 * i) : 0;
+  }
+  T* o = y + (r0 + lr) * ldy + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + lr + 4 * i >= rows) break;
+    const float s = mx4_scale_value<FMT>(sb[i]) * f;
+    float v[8];
+    e2m1x8_values(w[i], v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= s;
+    T* e = o + (long long)(4 * i) * ldy;
     if (vec && c + 8 <= cols) {
       if constexpr (sizeof(T) == 2) {
-        uint4 p;
-        p.x = pack_bf16x2(v[0], v[1]);
-        p.y = pack_bf16x2(v[2], v[3]);
-        p.z = pack_bf16x2(v[4], v[5]);
-        p.w = pack_bf16x2(v[6], v[7]);
-        *reinterpret_cast<uint4*>(o) = p;
+        uint4 b;
+        b.x = pack_bf16x2(v[0], v[1]);
+        b.y = pack_bf16x2(v[2], v[3]);
+        b.z = pack_bf16x2(v[4], v[5]);
+        b.w = pack_bf16x2(v[6], v[7]);
+        *reinterpret_cast<uint4*>(e) = b;
       } else {
-        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        reinterpret_cast<float4*>(e)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(e)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (c + k < cols) {
           if constexpr (sizeof(T) == 2)
-            o[k] = __float2bfloat16_rn(v[k]);
+            e[k] = __float2bfloat16_rn(v[k]);
           else
-            o[k] = v[k];
+            e[k] = v[k];
         }
     }
   }
@@ -466,36 +455,32 @@ unsigned grid_for(unsigned long long items, unsigned long long per_block, int nu
   return (unsigned)(want < most ? want : most);
 }
 
-// Tiles of 64 rows by 128 columns; the rows are covered up to a multiple of 128, so that the
-// transposed operand's padding is written.
-unsigned tile_grid(int rows, int cols) {
-  return (unsigned)((((long long)rows + 127) / 128) * (128 / kTR) * ((cols + kTC - 1) / kTC));
+// CTAs of a patch kernel: whole tiles of 128 rows, so that the transposed operand's padding is
+// written, and columns up to the next multiple of 128.
+unsigned tile_grid(int rows, int cols, int tile_cols) {
+  const long long kp = ((long long)cols + 127) & ~127ll;
+  return (unsigned)((((long long)rows + kTileRows - 1) / kTileRows) *
+                    ((kp + tile_cols - 1) / tile_cols));
 }
 
-template <typename T>
-cudaError_t quantize_t(int fmt, int rows, int cols, const T* x, long long ldx,
-                       const float* factor, const Mx4Out& out, const Mx4Out& out_t, int num_sms,
-                       cudaStream_t s) {
+template <int FMT, typename T>
+cudaError_t quantize_t(int rows, int cols, const T* x, long long ldx, const float* factor,
+                       const Mx4Out& out, const Mx4Out& out_t, cudaStream_t s) {
   const bool vec = row_vec(x, ldx, sizeof(T));
-  if (out_t.codes) {
-    const dim3 grid(tile_grid(rows, cols));
-    auto k = fmt == kMxfp4 ? mx4_both_kernel<kMxfp4, T> : mx4_both_kernel<kNvfp4, T>;
-    return launch_kernel(true, k, grid, dim3(256), 0, s, rows, cols, x, ldx, vec, factor, out,
-                         out_t);
-  }
-  const unsigned long long items = (unsigned long long)rows * ((cols + 255) / 256);
-  auto k = fmt == kMxfp4 ? mx4_rows_kernel<kMxfp4, T> : mx4_rows_kernel<kNvfp4, T>;
-  return launch_kernel(true, k, dim3(grid_for(items, 8, num_sms, 8)), dim3(256), 0, s, rows, cols,
-                       x, ldx, vec, factor, out);
+  auto k = !out_t.codes ? mx4_quantize_kernel<FMT, T, true, false>
+           : out.codes  ? mx4_quantize_kernel<FMT, T, true, true>
+                        : mx4_quantize_kernel<FMT, T, false, true>;
+  return launch_kernel(true, k, dim3(tile_grid(rows, cols, 64)), dim3(kTileThreads), 0, s, rows,
+                       cols, x, ldx, vec, factor, out, out_t);
 }
 
-template <typename T>
-cudaError_t dequantize_t(int fmt, int rows, int cols, const Mx4Out& q, const float* factor, T* y,
-                         long long ldy, int num_sms, cudaStream_t s) {
-  const unsigned long long n = (unsigned long long)rows * ((cols + 7) / 8);
-  auto k = fmt == kMxfp4 ? mx4_dequantize_kernel<kMxfp4, T> : mx4_dequantize_kernel<kNvfp4, T>;
-  return launch_kernel(true, k, dim3(grid_for(n, 256, num_sms, 8)), dim3(256), 0, s, rows, cols,
-                       (const uint8_t*)q.codes, (const uint8_t*)q.scales, q.ld, factor, y, ldy,
+template <int FMT, typename T>
+cudaError_t dequantize_t(int rows, int cols, const Mx4Out& q, const float* factor, T* y,
+                         long long ldy, cudaStream_t s) {
+  const long long tiles = (((long long)rows + kTileRows - 1) / kTileRows) * ((cols + 63) / 64);
+  return launch_kernel(true, mx4_dequantize_kernel<FMT, T>, dim3((unsigned)tiles),
+                       dim3(kTileThreads), 0, s, rows, cols, (const uint8_t*)q.codes,
+                       (const uint8_t*)q.scales, q.ld, factor, y, ldy,
                        row_vec(y, ldy, sizeof(T)));
 }
 
@@ -518,18 +503,25 @@ cudaError_t launch_mx4_factor(int dtype, int rows, int cols, const void* x, long
 
 cudaError_t launch_mx4_quantize(int fmt, int dtype, int rows, int cols, const void* x,
                                 long long ldx, const float* factor, const Mx4Out& out,
-                                const Mx4Out& out_t, int num_sms, cudaStream_t s) {
-  if (dtype)
-    return quantize_t(fmt, rows, cols, (const __nv_bfloat16*)x, ldx, factor, out, out_t, num_sms,
-                      s);
-  return quantize_t(fmt, rows, cols, (const float*)x, ldx, factor, out, out_t, num_sms, s);
+                                const Mx4Out& out_t, cudaStream_t s) {
+  const __nv_bfloat16* b = (const __nv_bfloat16*)x;
+  const float* f = (const float*)x;
+  if (fmt == kMxfp4)
+    return dtype ? quantize_t<kMxfp4>(rows, cols, b, ldx, factor, out, out_t, s)
+                 : quantize_t<kMxfp4>(rows, cols, f, ldx, factor, out, out_t, s);
+  return dtype ? quantize_t<kNvfp4>(rows, cols, b, ldx, factor, out, out_t, s)
+               : quantize_t<kNvfp4>(rows, cols, f, ldx, factor, out, out_t, s);
 }
 
 cudaError_t launch_mx4_dequantize(int fmt, int dtype, int rows, int cols, const Mx4Out& q,
-                                  const float* factor, void* y, long long ldy, int num_sms,
-                                  cudaStream_t s) {
-  if (dtype) return dequantize_t(fmt, rows, cols, q, factor, (__nv_bfloat16*)y, ldy, num_sms, s);
-  return dequantize_t(fmt, rows, cols, q, factor, (float*)y, ldy, num_sms, s);
+                                  const float* factor, void* y, long long ldy, cudaStream_t s) {
+  __nv_bfloat16* b = (__nv_bfloat16*)y;
+  float* f = (float*)y;
+  if (fmt == kMxfp4)
+    return dtype ? dequantize_t<kMxfp4>(rows, cols, q, factor, b, ldy, s)
+                 : dequantize_t<kMxfp4>(rows, cols, q, factor, f, ldy, s);
+  return dtype ? dequantize_t<kNvfp4>(rows, cols, q, factor, b, ldy, s)
+               : dequantize_t<kNvfp4>(rows, cols, q, factor, f, ldy, s);
 }
 
 cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* da,
@@ -537,17 +529,15 @@ cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* 
                                  const float* f_dut, const float* f_at, const Mx4Out& dg,
                                  const Mx4Out& dup, const Mx4Out& dgt, const Mx4Out& dupt,
                                  const Mx4Out& at, cudaStream_t s) {
+  const __nv_bfloat16* db = (const __nv_bfloat16*)da;
   const __nv_bfloat16* ub = (const __nv_bfloat16*)u;
   auto k = fmt == kMxfp4 ? mx4_gated_bwd_kernel<kMxfp4> : mx4_gated_bwd_kernel<kNvfp4>;
-  constexpr int smem = 3 * kTR * kTC * 4;
-  static SmemLimit limit[2];
-  cudaError_t e = limit[fmt].allow(k, smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(tile_grid(rows, F));
-  return launch_kernel(true, k, grid, dim3(256), (size_t)smem, s, rows, F, act,
-                       (const __nv_bfloat16*)da, ldda, row_vec(da, ldda, 2), ub, ldu,
-                       row_vec(u, ldu, 2), row_vec(ub + F, ldu, 2), f_du, f_dut, f_at, dg, dup,
-                       dgt, dupt, at);
+  auto vec = [](const void* p, long long ld) {  // loads of four bf16
+    return (reinterpret_cast<uintptr_t>(p) & 7) == 0 && ld % 4 == 0;
+  };
+  return launch_kernel(true, k, dim3(tile_grid(rows, F, 32)), dim3(kTileThreads), 0, s, rows, F,
+                       act, db, ldda, vec(db, ldda), ub, ldu, vec(ub, ldu), vec(ub + F, ldu), f_du,
+                       f_dut, f_at, dg, dup, dgt, dupt, at);
 }
 
 }  // namespace mgt

@@ -14,8 +14,8 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
 
-// Launches take 1-D grids of at most 2^31 - 1 blocks, one per 64 x 128 elements at least.
-constexpr int64_t kMostElements = (int64_t)1 << 43;
+// Launches take 1-D grids of at most 2^31 - 1 blocks, one per 128 x 32 elements at least.
+constexpr int64_t kMostElements = (int64_t)1 << 42;
 
 mgt_status check(const mgt_mx4* q) {
   if (!q->codes || !q->scales || q->rows < 1 || q->cols < 1) return MGT_EINVAL;
@@ -101,8 +101,9 @@ mgt_status mgt_mx4_quantize(int32_t dtype, const void* x, int64_t ldx, const mgt
   if (ldx < cols) return MGT_EINVAL;
   if (!dtype_ok(dtype) || !aligned(x, esz(dtype))) return MGT_EUNSUPPORTED;
   MX4_SMS(n);
+  (void)n;
   return status_of(launch_mx4_quantize(q ? q->format : qt->format, dtype == MGT_BF16, rows, cols,
-                                       x, ldx, factor_of(q ? q : qt), view(q), view(qt), n,
+                                       x, ldx, factor_of(q ? q : qt), view(q), view(qt),
                                        static_cast<cudaStream_t>(stream)));
 }
 
@@ -114,8 +115,9 @@ mgt_status mgt_mx4_dequantize(const mgt_mx4* q, int32_t dtype, void* y, int64_t 
   if (ldy < q->cols) return MGT_EINVAL;
   if (!dtype_ok(dtype) || !aligned(y, esz(dtype))) return MGT_EUNSUPPORTED;
   MX4_SMS(n);
+  (void)n;
   return status_of(launch_mx4_dequantize(q->format, dtype == MGT_BF16, q->rows, q->cols, view(q),
-                                         factor_of(q), y, ldy, n,
+                                         factor_of(q), y, ldy,
                                          static_cast<cudaStream_t>(stream)));
 }
 

@@ -154,6 +154,25 @@ __device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], const Mx4Blo
   return e2m1x8(v) & q.mask;
 }
 
+// Eight e2m1 codes to fp32.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{ .reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // Larger of two pairs of 16-bit values.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {

@@ -56,10 +56,9 @@ cudaError_t launch_mx4_factor(int dtype, int rows, int cols, const void* x, long
                               float* out, int num_sms, cudaStream_t s);
 cudaError_t launch_mx4_quantize(int fmt, int dtype, int rows, int cols, const void* x,
                                 long long ldx, const float* factor, const Mx4Out& out,
-                                const Mx4Out& out_t, int num_sms, cudaStream_t s);
+                                const Mx4Out& out_t, cudaStream_t s);
 cudaError_t launch_mx4_dequantize(int fmt, int dtype, int rows, int cols, const Mx4Out& q,
-                                  const float* factor, void* y, long long ldy, int num_sms,
-                                  cudaStream_t s);
+                                  const float* factor, void* y, long long ldy, cudaStream_t s);
 cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* da,
                                  long long ldda, const void* u, long long ldu, const float* f_du,
                                  const float* f_dut, const float* f_at, const Mx4Out& dg,
