@@ -80,6 +80,22 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// v = act(v)
+template <int N>
+__device__ __forceinline__ void gate_all(float (&v)[N], int act) {
+  float d;
+  if (act == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) gate_and_grad<0>(v[i], v[i], d);
+  } else if (act == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) gate_and_grad<1>(v[i], v[i], d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) gate_and_grad<2>(v[i], v[i], d);
+  }
+}
+
 constexpr int kStageK = 256;          // elements of K per stage: 128 bytes of a row
 constexpr int kPRows = 128;           // weight rows of a CTA's tile (per matrix)
 constexpr int kPBytes = kPRows * 128;
@@ -362,11 +378,10 @@ __global__ void __launch_bounds__(192)
         }
         float a[4];
         uint32_t mx = 0;
+        gate_all(v[0], g.act);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float h, dh;
-          gate_and_grad(v[0][i], g.act, h, dh);
-          a[i] = col + i < g.N ? h * v[NM - 1][i] : 0.f;  // columns behind the last are zeros
+          a[i] = col + i < g.N ? v[0][i] * v[NM - 1][i] : 0.f;  // columns behind the last are zeros
           mx = max(mx, abs_bits(a[i]));
         }
         constexpr int B = Mx4Fmt<FMT>::kBlock;
@@ -748,12 +763,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               store_block(my, w, g.u + g.N, g.ldu, row0, g.M, col0, g.N, g.width);
             }
           }
+          gate_all(v, g.act);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float h, dh;
-            gate_and_grad(v[k], g.act, h, dh);
-            v[k] = col0 + k < g.N ? h * w[k] : 0.f;  // columns behind the last are zeros
-          }
+          for (int k = 0; k < 32; ++k)
+            v[k] = col0 + k < g.N ? v[k] * w[k] : 0.f;  // columns behind the last are zeros
           constexpr int B = Mx4Fmt<FMT>::kBlock;
           uint32_t codes[4], bytes = 0;
 #pragma unroll

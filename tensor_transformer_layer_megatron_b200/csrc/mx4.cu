@@ -28,10 +28,6 @@ struct Vec8<__nv_bfloat16> {
     a = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ float at(int j) const {
-    const uint32_t w = j < 2 ? a.x : j < 4 ? a.y : j < 6 ? a.z : a.w;
-    return j & 1 ? bf16_hi(w) : bf16_lo(w);
-  }
   // Largest |x| as fp32 bits: bf16 magnitudes order like their bits, two to a word.
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t k = 0x7fff7fffu;
@@ -62,10 +58,6 @@ struct Vec8<float> {
     b = make_float4(v[4], v[5], v[6], v[7]);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ float at(int j) const {
-    return j < 4 ? (j < 2 ? (j ? a.y : a.x) : (j == 2 ? a.z : a.w))
-                 : (j < 6 ? (j == 4 ? b.x : b.y) : (j == 6 ? b.z : b.w));
-  }
   __device__ __forceinline__ uint32_t amax() const {
     return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
                max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
@@ -188,53 +180,7 @@ struct Patch {
   }
 };
 
-// Largest magnitude over the N lanes, a power of two, that share a block; `step` lanes apart.
-template <int N>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t m, int step) {
-#pragma unroll
-  for (int o = 1; o < N; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o * step));
-  return m;
-}
-
-// Codes of PC = 8 or 4 consecutive elements.
-template <int FMT, int PC>
-__device__ __forceinline__ uint32_t codes_of(const float (&v)[PC], const Mx4Block& q,
-                                             const Mx4Factor& f) {
-  if constexpr (PC == 8) {
-    return mx4_codes8<FMT>(v, q, f);
-  } else {
-    const float w[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
-    return mx4_codes8<FMT>(w, q, f);
-  }
-}
-
-// Row-wise operand: row i of the patch, v its PC elements, m their largest magnitude's bits.
-template <int FMT, int PC>
-__device__ __forceinline__ void put_row(const float (&v)[PC], uint32_t m, uint8_t* codes,
-                                        uint8_t* scale, bool ok, bool first, const Mx4Factor& f) {
-  const Mx4Block q = mx4_block<FMT>(lanes_max<Mx4Fmt<FMT>::kBlock / PC>(m, 1), f);
-  const uint32_t w = codes_of<FMT, PC>(v, q, f);
-  if (ok) {
-    if constexpr (PC == 8)
-      *reinterpret_cast<uint32_t*>(codes) = w;
-    else
-      *reinterpret_cast<uint16_t*>(codes) = (uint16_t)w;
-    if (first) *scale = (uint8_t)q.byte;
-  }
-}
-// Transposed operand: column j of the patch, v its eight elements.
-template <int FMT>
-__device__ __forceinline__ void put_col(const float (&v)[8], uint32_t m, uint8_t* codes,
-                                        uint8_t* scale, bool ok, bool first, const Mx4Factor& f) {
-  const Mx4Block q = mx4_block<FMT>(lanes_max<Mx4Fmt<FMT>::kBlock / 8>(m, 8), f);
-  const uint32_t w = mx4_codes8<FMT>(v, q, f);
-  if (ok) {
-    *reinterpret_cast<uint32_t*>(codes) = w;
-    if (first) *scale = (uint8_t)q.byte;
-  }
-}
-
-// Addresses of a patch in one operand: rows (columns) i of the patch follow each other by `ld / 2`
+// Addresses of a patch in one operand: rows (columns) i of the patch follow each other by `step`
 // bytes of codes and 16 bytes of scales (the eight lie in one group of 32).
 struct PatchOut {
   uint8_t *codes, *scale;
@@ -248,6 +194,211 @@ struct PatchOut {
   }
 };
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  return __byte_perm(a, b, sel);
+}
+
+// Largest magnitudes (fp32 bits) of CNT rows or columns over the N lanes, `step` apart, that share
+// a block. The upper halves of two of them travel in one word where they are enough: bf16 values
+// have no more, and an mxfp4 scale is read from the exponent.
+template <bool PACKED, int CNT, int N>
+__device__ __forceinline__ void lanes_max(uint32_t (&m)[CNT], int step) {
+  if constexpr (PACKED) {
+#pragma unroll
+    for (int i = 0; i < CNT; i += 2) {
+      uint32_t k = prmt(m[i], m[i + 1], 0x7632);
+#pragma unroll
+      for (int o = 1; o < N; o *= 2) k = max_u16x2(k, __shfl_xor_sync(0xffffffffu, k, o * step));
+      m[i] = k << 16;
+      m[i + 1] = k & 0xffff0000u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+#pragma unroll
+      for (int o = 1; o < N; o *= 2)
+        m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o * step));
+  }
+}
+
+// Patches: `pair` is elements (row i, columns 2 q and 2 q + 1), `each` replaces every element.
+struct PatchBf16 {
+  static constexpr int kCols = 8;
+  Vec8<__nv_bfloat16> w[8];
+  __device__ __forceinline__ uint32_t word(int i, int q) const {
+    return q == 0 ? w[i].a.x : q == 1 ? w[i].a.y : q == 2 ? w[i].a.z : w[i].a.w;
+  }
+  __device__ __forceinline__ uint64_t pair(int i, int q) const {
+    return f2_pack(bf16_lo(word(i, q)), bf16_hi(word(i, q)));
+  }
+  // Magnitudes two to a word: bf16 magnitudes order like their bits.
+  __device__ __forceinline__ void max_bits(uint32_t (&rm)[8], uint32_t (&cm)[8]) const {
+    uint32_t c[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        a[q] = word(i, q) & 0x7fff7fffu;
+        c[q] = max_u16x2(c[q], a[q]);
+      }
+      const uint32_t m = max_u16x2(max_u16x2(a[0], a[1]), max_u16x2(a[2], a[3]));
+      rm[i] = max(m << 16, m);  // only its upper half counts
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      cm[2 * q] = c[q] << 16;
+      cm[2 * q + 1] = c[q];
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F fn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t* a[4] = {&w[i].a.x, &w[i].a.y, &w[i].a.z, &w[i].a.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *a[q] = pack_bf16x2(fn(bf16_lo(*a[q])), fn(bf16_hi(*a[q])));
+    }
+  }
+};
+template <int PC>
+struct PatchF32 {
+  static constexpr int kCols = PC;
+  float v[8][PC];
+  __device__ __forceinline__ uint64_t pair(int i, int q) const {
+    return f2_pack(v[i][2 * q], v[i][2 * q + 1]);
+  }
+  __device__ __forceinline__ void max_bits(uint32_t (&rm)[8], uint32_t (&cm)[PC]) const {
+#pragma unroll
+    for (int j = 0; j < PC; ++j) cm[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      rm[i] = 0;
+#pragma unroll
+      for (int j = 0; j < PC; ++j) {
+        const uint32_t b = abs_bits(v[i][j]);
+        rm[i] = max(rm[i], b);
+        cm[j] = max(cm[j], b);
+      }
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F fn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < PC; ++j) v[i][j] = fn(v[i][j]);
+  }
+};
+
+// A pair scaled by a pair (mxfp4: exact; nvfp4: with the residual correction of mx4_scaled).
+template <int FMT>
+__device__ __forceinline__ void scaled2(uint64_t x, uint64_t inv, uint64_t neg_fs, float& a,
+                                        float& b) {
+  uint64_t y = f2_mul(x, inv);
+  if constexpr (FMT == kNvfp4) y = f2_fma(f2_fma(y, neg_fs, x), inv, y);
+  f2_unpack(y, a, b);
+}
+
+// Quantise a patch along its rows (into `out`) and / or its columns (into `out_t`); an operand
+// without codes is left out.
+template <int FMT, bool PACKED, bool ROWS, bool COLS, typename P>
+__device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, int cols, int kp,
+                                               const Mx4Out& out, const Mx4Out& out_t, Mx4Factor f,
+                                               Mx4Factor ft) {
+  constexpr int B = Mx4Fmt<FMT>::kBlock, PC = P::kCols;
+  uint32_t rm[8], cm[PC];
+  x.max_bits(rm, cm);
+  if constexpr (ROWS) lanes_max<PACKED, 8, B / PC>(rm, 1);
+  if constexpr (COLS) lanes_max<PACKED, PC, B / 8>(cm, 8);
+  if constexpr (FMT == kNvfp4) {
+    // Rare: a kept factor far too small (elements beyond 4096 f saturate wherever they lie, so
+    // they may be cut off there before a quotient overflows), or a factor so small that f s would
+    // be subnormal (everything times 2^64).
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
+    const float f0 = ROWS && COLS ? fmaxf(f.f, ft.f) : ROWS ? f.f : ft.f;
+    const bool tiny = (ROWS && f.tiny) || (COLS && ft.tiny);
+    if (tiny || m > __float_as_uint(4096.0f * f0)) {
+      const float lim = 4096.0f * f0, k = tiny ? 1.8446744e19f : 1.0f;
+      auto cut = [&](float v) { return fminf(fmaxf(v, -lim), lim) * k; };
+      auto cut_bits = [&](uint32_t b) {
+        return b >= 0x7f800000u ? b : __float_as_uint(fminf(__uint_as_float(b), lim) * k);
+      };
+      x.each(cut);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rm[i] = cut_bits(rm[i]);
+#pragma unroll
+      for (int j = 0; j < PC; ++j) cm[j] = cut_bits(cm[j]);
+      f.f *= k;
+      f.inv *= 1.0f / k;
+      ft.f *= k;
+      ft.inv *= 1.0f / k;
+    }
+  }
+  const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c), t = PatchOut::of<FMT>(out_t, p.c, p.r);
+  const bool put_rows = ROWS && out.codes && p.c < kp;
+  uint64_t cinv[PC / 2], cfs[PC / 2];
+  uint32_t cc[PC], cmask[PC];
+  if constexpr (COLS) {
+#pragma unroll
+    for (int q = 0; q < PC / 2; ++q) {
+      const Mx4Block a = mx4_block<FMT>(cm[2 * q], ft), b = mx4_block<FMT>(cm[2 * q + 1], ft);
+      cinv[q] = f2_pack(a.inv, b.inv);
+      cfs[q] = f2_pack(-a.fs, -b.fs);
+      cmask[2 * q] = a.mask;
+      cmask[2 * q + 1] = b.mask;
+      if (out_t.codes && t.first) {
+        if (p.c + 2 * q < cols) t.scale[32 * q] = (uint8_t)a.byte;
+        if (p.c + 2 * q + 1 < cols) t.scale[32 * q + 16] = (uint8_t)b.byte;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if constexpr (ROWS) {
+        const Mx4Block s = mx4_block<FMT>(rm[i + h], f);
+        const uint64_t inv = f2_pack(s.inv, s.inv), fs = f2_pack(-s.fs, -s.fs);
+        float e[8];
+#pragma unroll
+        for (int q = 0; q < PC / 2; ++q)
+          scaled2<FMT>(x.pair(i + h, q), inv, fs, e[2 * q], e[2 * q + 1]);
+        if (put_rows && p.r + i + h < rows) {
+          uint8_t* d = o.codes + (i + h) * o.step;
+          if constexpr (PC == 8)
+            *reinterpret_cast<uint32_t*>(d) = e2m1x8(e) & s.mask;
+          else
+            *reinterpret_cast<uint16_t*>(d) =
+                (uint16_t)((e2m1x2(e[0], e[1]) | (e2m1x2(e[2], e[3]) << 8)) & s.mask);
+          if (o.first) o.scale[16 * (i + h)] = (uint8_t)s.byte;
+        }
+      }
+    if constexpr (COLS) {
+#pragma unroll
+      for (int q = 0; q < PC / 2; ++q) {
+        float a0, a1, b0, b1;
+        scaled2<FMT>(x.pair(i, q), cinv[q], cfs[q], a0, a1);
+        scaled2<FMT>(x.pair(i + 1, q), cinv[q], cfs[q], b0, b1);
+        const uint32_t w0 = e2m1x2(a0, b0), w1 = e2m1x2(a1, b1);
+        const uint32_t sel = i == 2 ? 0x3240 : i == 4 ? 0x3410 : 0x4210;
+        cc[2 * q] = i ? prmt(cc[2 * q], w0, sel) : w0;
+        cc[2 * q + 1] = i ? prmt(cc[2 * q + 1], w1, sel) : w1;
+      }
+    }
+  }
+  if constexpr (COLS) {
+    if (out_t.codes) {
+#pragma unroll
+      for (int j = 0; j < PC; ++j)
+        if (p.c + j < cols)
+          *reinterpret_cast<uint32_t*>(t.codes + j * t.step) = cc[j] & cmask[j];
+    }
+  }
+}
+
 template <int FMT, typename T, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kTileThreads)
     mx4_quantize_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
@@ -256,33 +407,23 @@ __global__ void __launch_bounds__(kTileThreads)
   const Patch p = Patch::of<8>(cols);
   if (!COLS && p.r - (threadIdx.x & 24) >= rows) return;  // the whole warp is behind the last row
   const int kp = (cols + 127) & ~127;
-  Vec8<T> w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) load8(w[i], x + (p.r + i) * ldx, p.c, cols, p.r + i < rows, vec);
   const Mx4Factor f = mx4_factor<FMT>(factor);
-  if constexpr (ROWS) {
-    const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c);
+  constexpr bool kPacked = FMT == kMxfp4 || sizeof(T) == 2;
+  if constexpr (sizeof(T) == 2) {
+    PatchBf16 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      load8(v.w[i], x + (p.r + i) * ldx, p.c, cols, p.r + i < rows, vec);
+    quantize_patch<FMT, kPacked, ROWS, COLS>(v, p, rows, cols, kp, out, out_t, f, f);
+  } else {
+    PatchF32<8> v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v[8];
-      w[i].get(v);
-      put_row<FMT, 8>(v, w[i].amax(), o.codes + i * o.step, o.scale + 16 * i,
-                      p.r + i < rows && p.c < kp, o.first, f);
+      Vec8<T> w;
+      load8(w, x + (p.r + i) * ldx, p.c, cols, p.r + i < rows, vec);
+      w.get(v.v[i]);
     }
-  }
-  if constexpr (COLS) {
-    const PatchOut o = PatchOut::of<FMT>(out_t, p.c, p.r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v[8];
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = w[i].at(j);
-        m = max(m, abs_bits(v[i]));
-      }
-      put_col<FMT>(v, m, o.codes + j * o.step, o.scale + 16 * j, p.c + j < cols, o.first, f);
-    }
+    quantize_patch<FMT, kPacked, ROWS, COLS>(v, p, rows, cols, kp, out, out_t, f, f);
   }
 }
 
@@ -312,37 +453,9 @@ struct Quad {  // four consecutive bf16
   }
 };
 
-template <int FMT>
-__device__ __forceinline__ void put_patch_rows(const float (&v)[8][4], const Mx4Out& out,
-                                               const Patch& p, int rows, const Mx4Factor& f) {
-  const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = max(max(abs_bits(v[i][0]), abs_bits(v[i][1])),
-                           max(abs_bits(v[i][2]), abs_bits(v[i][3])));
-    put_row<FMT, 4>(v[i], m, o.codes + i * o.step, o.scale + 16 * i, p.r + i < rows, o.first, f);
-  }
-}
-template <int FMT>
-__device__ __forceinline__ void put_patch_cols(const float (&v)[8][4], const Mx4Out& out,
-                                               const Patch& p, int cols, const Mx4Factor& f) {
-  const PatchOut o = PatchOut::of<FMT>(out, p.c, p.r);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float c[8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = v[i][j];
-      m = max(m, abs_bits(c[i]));
-    }
-    put_col<FMT>(c, m, o.codes + j * o.step, o.scale + 16 * j, p.c + j < cols, o.first, f);
-  }
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(kTileThreads)
-    mx4_gated_bwd_kernel(int rows, int F, int act, const __nv_bfloat16* __restrict__ da,
+template <int FMT, int ACT>
+__global__ void __launch_bounds__(kTileThreads, 4)
+    mx4_gated_bwd_kernel(int rows, int F, const __nv_bfloat16* __restrict__ da,
                          long long ldda, bool vec_da, const __nv_bfloat16* __restrict__ u,
                          long long ldu, bool vec_g, bool vec_u, const float* __restrict__ f_du,
                          const float* __restrict__ f_dut, const float* __restrict__ f_at,
@@ -357,29 +470,39 @@ __global__ void __launch_bounds__(kTileThreads)
     wg[i].load(u + row * ldu, p.c, F, row < rows, vec_g);
     wu[i].load(u + row * ldu + F, p.c, F, row < rows, vec_u);
   }
-  float g[8][4], q[8][4], a[8][4];
+  const Mx4Factor fr = mx4_factor<FMT>(dg.codes ? f_du : nullptr);
+  const Mx4Factor fc = mx4_factor<FMT>(dgt.codes ? f_dut : nullptr);
+  const Mx4Factor fa = mx4_factor<FMT>(at.codes ? f_at : nullptr);
+  const int kp = (F + 127) & ~127;
+  // One result at a time: its 32 values and the inputs fit the registers of four CTAs per SM. The
+  // activation is computed again for each, which costs less than holding three results.
+  PatchF32<4> v;
+  auto result = [&](auto fn) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float h, dh;
-      gate_and_grad(wg[i].at(j), act, h, dh);
-      const float d = wd[i].at(j), up = wu[i].at(j);
-      g[i][j] = d * up * dh;
-      q[i][j] = d * h;
-      a[i][j] = h * up;
+    for (int i = 0; i < 8; ++i) {  // (as if changed, or the compiler keeps the activations after all)
+      asm volatile("" : "+r"(wg[i].a.x));
+      asm volatile("" : "+r"(wg[i].a.y));
     }
-  if (dg.codes) {
-    const Mx4Factor f = mx4_factor<FMT>(f_du);
-    put_patch_rows<FMT>(g, dg, p, rows, f);
-    put_patch_rows<FMT>(q, dup, p, rows, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float h, dh;
+        gate_and_grad<ACT>(wg[i].at(j), h, dh);
+        v.v[i][j] = fn(wd[i].at(j), wu[i].at(j), h, dh);
+      }
+  };
+  constexpr bool kPacked = FMT == kMxfp4;
+  if (dg.codes || dgt.codes) {
+    result([](float d, float up, float, float dh) { return d * up * dh; });
+    quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dg, dgt, fr, fc);
+    result([](float d, float, float h, float) { return d * h; });
+    quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dup, dupt, fr, fc);
   }
-  if (dgt.codes) {
-    const Mx4Factor f = mx4_factor<FMT>(f_dut);
-    put_patch_cols<FMT>(g, dgt, p, F, f);
-    put_patch_cols<FMT>(q, dupt, p, F, f);
+  if (at.codes) {
+    result([](float, float up, float h, float) { return h * up; });
+    quantize_patch<FMT, kPacked, false, true>(v, p, rows, F, kp, at, at, fa, fa);
   }
-  if (at.codes) put_patch_cols<FMT>(a, at, p, F, mx4_factor<FMT>(f_at));
 }
 
 // ---------------------------------------------------------------------------- and back
@@ -531,12 +654,17 @@ cudaError_t launch_mx4_gated_bwd(int fmt, int act, int rows, int F, const void* 
                                  const Mx4Out& at, cudaStream_t s) {
   const __nv_bfloat16* db = (const __nv_bfloat16*)da;
   const __nv_bfloat16* ub = (const __nv_bfloat16*)u;
-  auto k = fmt == kMxfp4 ? mx4_gated_bwd_kernel<kMxfp4> : mx4_gated_bwd_kernel<kNvfp4>;
+  auto k = fmt == kMxfp4 ? (act == 0   ? mx4_gated_bwd_kernel<kMxfp4, 0>
+                            : act == 1 ? mx4_gated_bwd_kernel<kMxfp4, 1>
+                                       : mx4_gated_bwd_kernel<kMxfp4, 2>)
+                         : (act == 0   ? mx4_gated_bwd_kernel<kNvfp4, 0>
+                            : act == 1 ? mx4_gated_bwd_kernel<kNvfp4, 1>
+                                       : mx4_gated_bwd_kernel<kNvfp4, 2>);
   auto vec = [](const void* p, long long ld) {  // loads of four bf16
     return (reinterpret_cast<uintptr_t>(p) & 7) == 0 && ld % 4 == 0;
   };
   return launch_kernel(true, k, dim3(tile_grid(rows, F, 32)), dim3(kTileThreads), 0, s, rows, F,
-                       act, db, ldda, vec(db, ldda), ub, ldu, vec(ub, ldu), vec(ub + F, ldu), f_du,
+                       db, ldda, vec(db, ldda), ub, ldu, vec(ub, ldu), vec(ub + F, ldu), f_du,
                        f_dut, f_at, dg, dup, dgt, dupt, at);
 }
 

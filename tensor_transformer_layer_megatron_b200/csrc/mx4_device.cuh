@@ -126,6 +126,15 @@ __device__ __forceinline__ float mx4_scaled_wide(float x, uint32_t byte, float i
          mx4_scale_value<kNvfp4>(byte);
 }
 
+// Two fp32 values to two codes in the low byte (lo in its low half).
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{ .reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b; }"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+
 // Eight fp32 values to eight e2m1 codes (round to nearest, ties to even, saturating at 6), the
 // first in the low four bits.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
@@ -181,15 +190,16 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Activation of a gated block and its derivative. act: 0 silu, 1 gelu (erf), 2 gelu (tanh). A
+// Activation of a gated block and its derivative. ACT: 0 silu, 1 gelu (erf), 2 gelu (tanh). A
 // block's scale follows its largest value, so a value counts by its relative error however small
 // it is: Phi(z) = erfc(-z / sqrt 2) / 2 and (1 + tanh y) / 2 = 1 / (1 + e^-2y) keep it in the
 // negative tail, where 1 + erf and 1 + tanh cancel.
-__device__ __forceinline__ void gate_and_grad(float z, int act, float& h, float& dh) {
-  if (act == 0) {
+template <int ACT>
+__device__ __forceinline__ void gate_and_grad(float z, float& h, float& dh) {
+  if constexpr (ACT == 0) {
     // e^-z and the reciprocal from the special-function unit (relative error about 2^-21 + |z| 2^-24)
     silu_and_grad_bf16out(z, h, dh);
-  } else if (act == 1) {
+  } else if constexpr (ACT == 1) {
     const float c = 0.5f * erfcf(z * -0.7071067811865476f);
     h = z * c;
     dh = fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), c);
