@@ -420,7 +420,7 @@ struct PairArgs {
   void* C;
   int c_f32;
   long long ldc;
-  int width;                // bytes per store that C's (u's) alignment allows: 16, 4 or 2
+  bool tma;                 // C (u) takes bulk tensor stores
   int up_tiles;             // gated: scale tiles of rows before the first up row
   int act;
   Mx4Out a;
@@ -434,7 +434,7 @@ constexpr int kPairThreads = 320;
 constexpr int kSlotCols = 24;
 constexpr int kAcc1 = 192;     // first column of the second accumulator
 constexpr int kScaleCol = 448;
-constexpr int kStoreBytes = 32 * 144;  // staging of one warp: 32 rows of at most 128 bytes, padded
+constexpr int kStoreBytes = 5120;  // staging of one warp: 32 rows of at most 144 bytes, in whole KB
 
 template <int FMT>
 struct PairCfg {
@@ -459,52 +459,92 @@ __device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint32_t smem_
                "l"(scale_desc(smem_addr))
                : "memory");
 }
-// A warp's 32 rows by 32 columns (thread = row) to global memory through its staging buffer, so
-// that consecutive lanes write consecutive bytes of a row. T: bf16 or fp32; width: bytes per lane.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0,
+                                             int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// A warp's 32 rows by 32 columns (thread = row) to global memory through its staging buffer.
+// Where the output's alignment allows it (map), by a bulk tensor store: bf16 blocks (2 KB) use two
+// halves of the buffer in turn (`turn`), fp32 blocks (4 KB) all of it, 16-byte units of a row
+// permuted as the map's swizzle has it.
 template <typename T>
-__device__ __forceinline__ void store_block(uint8_t* stg, const float (&v)[32], T* base,
-                                            long long ld, int row0, int rows, int col0, int cols,
-                                            int width) {
+__device__ __forceinline__ void store_block_tma(uint8_t* stg, int& turn, const float (&v)[32],
+                                                const CUtensorMap* map, int row0, int col0) {
   const int lane = threadIdx.x & 31;
-  constexpr int kRow = 32 * (int)sizeof(T) + 16;  // 16-byte accesses of eight rows meet no bank twice
+  constexpr int kRow = 32 * (int)sizeof(T), kUnits = kRow / 16;
+  uint8_t* buf = stg;
   if constexpr (sizeof(T) == 2) {
+    buf += (turn & 1) * 2048;
+    ++turn;
+  }
+  if (lane == 0) {  // the buffer's last store has read it
+    if constexpr (sizeof(T) == 2)
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    else
+      bulk_wait_read0();
+  }
+  __syncwarp();
+  const int swz = sizeof(T) == 2 ? (lane >> 1) & 3 : lane & 7;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(stg + lane * kRow + i * 16) =
-          make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-  } else {
+  for (int i = 0; i < kUnits; ++i) {
+    uint4 w;
+    if constexpr (sizeof(T) == 2)
+      w = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                     pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    else
+      w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    *reinterpret_cast<uint4*>(buf + lane * kRow + ((i ^ swz) << 4)) = w;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, buf, col0, row0);
+    bulk_commit();
+  }
+}
+// Elsewhere by stores in which consecutive lanes write consecutive elements of a row.
+template <typename T>
+__device__ __forceinline__ void store_block_any(uint8_t* stg, const float (&v)[32], T* base,
+                                                long long ld, int row0, int rows, int col0,
+                                                int cols) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kRow = 32 * (int)sizeof(T) + 16;  // eight rows' 16-byte units meet no bank twice
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(stg + lane * kRow + i * 16) =
-          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
+    uint4 w;
+    if constexpr (sizeof(T) == 2)
+      w = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                     pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    else
+      w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    *reinterpret_cast<uint4*>(stg + lane * kRow + i * 16) = w;
   }
   __syncwarp();
   T* out = base + (long long)row0 * ld + col0;
   const int nr = min(32, rows - row0), nc = min(32, cols - col0);
-  if (width == 16) {
-    constexpr int kLanes = 32 * sizeof(T) / 16, kElems = 16 / sizeof(T);
-    const int c = (lane % kLanes) * kElems;
-#pragma unroll
-    for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
-      const uint4 w = *reinterpret_cast<const uint4*>(stg + r * kRow + c * sizeof(T));
-      if (r < nr) {
-        if (c + kElems <= nc) {
-          *reinterpret_cast<uint4*>(out + (long long)r * ld + c) = w;
-        } else {
-          const T* e = reinterpret_cast<const T*>(stg + r * kRow);
-          for (int i = c; i < nc; ++i) out[(long long)r * ld + i] = e[i];
-        }
-      }
-    }
-  } else {
 #pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const T e = reinterpret_cast<const T*>(stg + r * kRow)[lane];
-      if (r < nr && lane < nc) out[(long long)r * ld + lane] = e;
-    }
+  for (int r = 0; r < 32; ++r) {
+    const T e = reinterpret_cast<const T*>(stg + r * kRow)[lane];
+    if (r < nr && lane < nc) out[(long long)r * ld + lane] = e;
   }
   __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void store_block(uint8_t* stg, int& turn, const float (&v)[32],
+                                            const CUtensorMap* map, T* base, long long ld, int row0,
+                                            int rows, int col0, int cols, bool tma) {
+  if (tma)
+    store_block_tma<T>(stg, turn, v, map, row0, col0);
+  else
+    store_block_any(stg, v, base, ld, row0, rows, col0, cols);
 }
 
 template <int FMT, bool GATED>
@@ -512,7 +552,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB2,
                     const __grid_constant__ CUtensorMap tmSA,
-                    const __grid_constant__ CUtensorMap tmSB, const PairArgs g) {
+                    const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ CUtensorMap tmO,
+                    const __grid_constant__ CUtensorMap tmO2, const PairArgs g) {
   using C = PairCfg<FMT>;
   constexpr int S = C::kStages, kTps = C::kTps;
   constexpr int kChunks = FMT == kMxfp4 ? 1 : 2;      // scale slots per stage
@@ -520,9 +562,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   constexpr int kStepsPerChunk = 4 / kChunks;         // products of 64 elements per chunk
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sf = smem + S * C::kOperandBytes;
-  uint8_t* stg = sf + S * C::kScaleBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg + 8 * kStoreBytes);
+  uint8_t* stg = smem + S * C::kOperandBytes;
+  uint8_t* sf = stg + 8 * kStoreBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf + S * C::kScaleBytes);
   uint64_t* empty = full + S;
   uint64_t* slot_free = empty + S;
   uint64_t* tfull = slot_free + 2;
@@ -706,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const Mx4Factor of = mx4_factor<FMT>(GATED ? g.out_factor : nullptr);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t overlap0 = mapa_shared(smem_u32(overlap), 0);
-    int acc = 0;
+    int acc = 0, turn = 0;
     uint32_t acc_phase = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
       const int row0 = tile_m(tile) * 256 + (int)rank * 128 + ew * 32;
@@ -716,27 +758,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const uint32_t t0 = tmem + (acc ? kAcc1 : 0) + ((uint32_t)(ew * 32) << 16);
       if constexpr (!GATED) {
-        // 32-column chunks; the first one lies in the columns common to both accumulators (6, 7
-        // of the first, 0, 1 of the second)
-#pragma unroll 1
+        // Four 32-column chunks per warp; the first lies in the columns common to both
+        // accumulators (6, 7 of the first, 0, 1 of the second). All are read into registers before
+        // any is stored.
+        uint32_t r[4][32];
+        auto chunk = [&](int i) {
+          return acc ? (i == 0 ? set : 1 + 3 * set + i) : (i == 0 ? 6 + set : 3 * set + i - 1);
+        };
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int c = acc ? (i == 0 ? set : 1 + 3 * set + i) : (i == 0 ? 6 + set : 3 * set + i - 1);
-          float v[32];
-          tmem_ld_32x32b_x32(t0 + c * 32, v);
+          tmem_ld_32x32b_x32_nw(t0 + chunk(i) * 32, r[i]);
           if (i == 0 || i == 3) {
+            tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(i == 0 ? overlap0 : tempty0 + acc * 8);
           }
-          const int col0 = nt * 256 + c * 32;
-          if (col0 < g.N && row0 < g.M) {
+        }
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= f;
+        for (int i = 0; i < 4; ++i) {
+          reg_fence(r[i]);
+          const int col0 = nt * 256 + chunk(i) * 32;
+          if (col0 < g.N && row0 < g.M) {
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[i][k]) * f;
             if (g.c_f32)
-              store_block(my, v, static_cast<float*>(g.C), g.ldc, row0, g.M, col0, g.N, g.width);
+              store_block(my, turn, v, &tmO, static_cast<float*>(g.C), g.ldc, row0, g.M, col0, g.N,
+                          g.tma);
             else
-              store_block(my, v, static_cast<__nv_bfloat16*>(g.C), g.ldc, row0, g.M, col0, g.N,
-                          g.width);
+              store_block(my, turn, v, &tmO, static_cast<__nv_bfloat16*>(g.C), g.ldc, row0, g.M,
+                          col0, g.N, g.tma);
           }
         }
       } else {
@@ -759,8 +811,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           if (g.u && row0 < g.M) {
             if (col0 < g.N) {
-              store_block(my, v, g.u, g.ldu, row0, g.M, col0, g.N, g.width);
-              store_block(my, w, g.u + g.N, g.ldu, row0, g.M, col0, g.N, g.width);
+              store_block(my, turn, v, &tmO, g.u, g.ldu, row0, g.M, col0, g.N, g.tma);
+              store_block(my, turn, w, &tmO2, g.u + g.N, g.ldu, row0, g.M, col0, g.N, g.tma);
             }
           }
           gate_all(v, g.act);
@@ -801,6 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   }
+  if (warp >= 2 && lane == 0) bulk_wait0();  // the stores have left the staging buffers
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -893,10 +946,6 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, tp, tp2, tq, a);
 }
 
-int store_width(const void* p, long long ld, int esz) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0 ? 16 : esz;
-}
-
 template <int FMT, bool GATED>
 cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   using C = PairCfg<FMT>;
@@ -922,10 +971,17 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   a.up_tiles = up0 / 128;
   a.act = g.act; a.a = g.a; a.out_factor = g.out_factor;
   a.u = static_cast<__nv_bfloat16*>(g.u); a.ldu = g.ldu;
+  // Bulk tensor stores need 16-byte aligned bases and row strides; u's second half starts at
+  // column N.
+  CUtensorMap to = {}, to2 = {};
+  auto out_map = [&](CUtensorMap* m, void* p, long long ld, int esz) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0 &&
+           make_tensor_map_out_2d(m, p, (uint64_t)g.N, (uint64_t)g.M, (uint64_t)ld, esz == 4);
+  };
   if (GATED)
-    a.width = (g.N % 8) ? 2 : store_width(g.u, g.ldu, 2);
+    a.tma = a.u && out_map(&to, a.u, g.ldu, 2) && out_map(&to2, a.u + g.N, g.ldu, 2);
   else
-    a.width = store_width(g.C, g.ldc, g.c_f32 ? 4 : 2);
+    a.tma = out_map(&to, g.C, g.ldc, g.c_f32 ? 4 : 2);
   a.err = g.err;
   auto kern = mx4_pair_kernel<FMT, GATED>;
   static SmemLimit limit;
@@ -934,7 +990,7 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   const int tiles = a.num_m * a.num_n;
   const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
   return launch_kernel(true, kern, dim3(2 * pairs), dim3(kPairThreads), (size_t)C::kSmem, s, ta, tb,
-                       tb2, tsa, tsb, a);
+                       tb2, tsa, tsb, to, to2, a);
 }
 
 template <int FMT, bool GATED>

@@ -1080,6 +1080,21 @@ bool make_tensor_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uin
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_out_2d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t ld,
+                            bool f32) {
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  const int esz = f32 ? 4 : 2;
+  cuuint64_t gd[2] = {cols, rows};
+  cuuint64_t gs[1] = {ld * esz};
+  cuuint32_t bd[2] = {32, 32};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
+            gd, gs, bd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 bool make_map(CUtensorMap* m, const void* base, const uint64_t dims[3], const uint64_t strides[2],

@@ -139,6 +139,10 @@ bool make_tensor_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uin
 // box_tiles tiles, unswizzled, zero fill out of bounds.
 bool make_tensor_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t rows,
                            uint64_t ld, uint32_t box_tiles);
+// Output map {cols, rows}, row stride ld elements, box 32 x 32; fp32 with 128-byte, bf16 with
+// 64-byte swizzle.
+bool make_tensor_map_out_2d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t ld,
+                            bool f32);
 
 // tcgen05 / TMA GEMM for bf16 operands (fp32 accumulate in tensor memory).
 // Builds the tensor maps from the pointers in `args` (A, B, strides) and launches a persistent
