@@ -23,6 +23,14 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap* m, uint64_t* bar,
       : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // A 512-byte scale tile (128 rows by 4 blocks) to four tensor-memory columns: lane r % 32 of
 // column r / 32 gets the four bytes of row r, in all four lane quarters. The source is 32 rows
 // of 16 bytes, unswizzled: core matrices of 8 rows, 128 bytes apart.
@@ -99,6 +107,7 @@ __device__ __forceinline__ void gate_all(float (&v)[N], int act) {
 constexpr int kStageK = 256;          // elements of K per stage: 128 bytes of a row
 constexpr int kPRows = 128;           // weight rows of a CTA's tile (per matrix)
 constexpr int kPBytes = kPRows * 128;
+constexpr int kPrefetchStages = 8;    // stages fetched into L2 ahead: 128 KB a CTA
 
 // ---------------------------------------------------------------------------- weights as rows
 // The weights' rows take the 128 lanes of the accumulator and up to 256 tokens its columns, so a
@@ -187,6 +196,16 @@ __global__ void __launch_bounds__(192)
   // groups of 128 tokens that have scales in the buffer
   const int q_groups = min(groups, (g.M - q0 + 127) / 128);
 
+  if (warp == 2 && lane == 0) {
+    // The weights' first stages into L2 while the previous kernel still runs. It may be the one
+    // that writes them: L2 then takes its writes, and the copies to shared memory come after
+    // grid_dependency_wait.
+    const int end = min(k_end, k_begin + kPrefetchStages);
+    for (int kt = k_begin; kt < end; ++kt) {
+      tma_prefetch_2d(&tmP, kt * 128, p0);
+      if (GATED) tma_prefetch_2d(&tmP2, kt * 128, p0);
+    }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -208,6 +227,7 @@ __global__ void __launch_bounds__(192)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t acc_cols = (uint32_t)(g.bnq + 31) & ~31u;
+  launch_dependents();
   grid_dependency_wait();  // the operands are the previous kernel's results
 
   if (warp == 0) {
@@ -416,6 +436,7 @@ __global__ void __launch_bounds__(192)
 struct PairArgs {
   int M, N, kp;
   int num_m, num_n, m_fast;
+  int bn;                   // columns of a tile: 256 or 128
   const float *a_factor, *b_factor;
   void* C;
   int c_f32;
@@ -430,17 +451,24 @@ struct PairArgs {
   int* err;
 };
 
+// Arrive on a barrier of the pair without ordering this thread's stores before it: the epilogue
+// only reports tensor memory that it has read (tcgen05.wait::ld), and a releasing arrive waited
+// 1500 cycles for the stores of the tile before.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 constexpr int kPairThreads = 320;
-constexpr int kSlotCols = 24;
-constexpr int kAcc1 = 192;     // first column of the second accumulator
 constexpr int kScaleCol = 448;
+constexpr int kSlotCols = 24;
 constexpr int kStoreBytes = 5120;  // staging of one warp: 32 rows of at most 144 bytes, in whole KB
 
 template <int FMT>
 struct PairCfg {
   static constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;
   static constexpr int kStages = FMT == kMxfp4 ? 5 : 4;
-  static constexpr int kScaleBytes = 3 * kTps * 512;
+  static constexpr int kScaleBytes = 3 * kTps * 512;  // A's 128 rows and B's 256
   static constexpr int kOperandBytes = 2 * 128 * 128;
   static constexpr int kStageBytes = kOperandBytes + kScaleBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kStoreBytes + 512;
@@ -612,6 +640,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();  // the operands are the previous kernel's results
 
+  const int bn = GATED ? 256 : g.bn, sb = bn / 128;
+  const bool shared_cols = bn == 256;            // the accumulators overlap
+  const uint32_t acc1 = shared_cols ? 192 : bn;  // first column of the second
   auto tile_m = [&](int t) { return g.m_fast ? t % g.num_m : t / g.num_n; };
   auto tile_n = [&](int t) { return g.m_fast ? t / g.num_m : t % g.num_n; };
 
@@ -623,13 +654,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
       const int m0 = tile_m(tile) * 256 + (int)rank * 128;
       const int nt = tile_n(tile);
-      const int sb0 = GATED ? nt : 2 * nt, sb1 = GATED ? g.up_tiles + nt : 2 * nt + 1;
+      const int sb0 = GATED ? nt : nt * bn / 128;
+      const uint32_t stage_tx = 2 * (128 * 128 + bn / 2 * 128 + (1 + sb) * kTps * 512);
       for (int kt = 0; kt < ki; ++kt) {
         if (!mbar_wait(&empty[stage], phase ^ 1, g.err, kErrTimeoutProducer, abort_flag)) {
           ok = false;
           break;
         }
-        if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+        if (leader) mbar_arrive_expect_tx(&full[stage], stage_tx);
         const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
         uint8_t* d = smem + stage * C::kOperandBytes;
         uint8_t* s = sf + stage * C::kScaleBytes;
@@ -637,10 +669,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (GATED)
           tma_load_2d_pair(rank ? &tmB2 : &tmB, fb, d + 128 * 128, kt * 128, nt * 128);
         else
-          tma_load_2d_pair(&tmB, fb, d + 128 * 128, kt * 128, nt * 256 + (int)rank * 128);
+          tma_load_2d_pair(&tmB, fb, d + 128 * 128, kt * 128, nt * bn + (int)rank * (bn / 2));
         tma_load_3d_pair(&tmSA, fb, s, 0, kt * kTps, m0 / 128);
-        tma_load_3d_pair(&tmSB, fb, s + kTps * 512, 0, kt * kTps, sb0);
-        tma_load_3d_pair(&tmSB, fb, s + 2 * kTps * 512, 0, kt * kTps, sb1);
+        for (int q = 0; q < sb; ++q)
+          tma_load_3d_pair(&tmSB, fb, s + (1 + q) * kTps * 512, 0, kt * kTps,
+                           GATED && q ? g.up_tiles + nt : sb0 + q);
         if (++stage == S) {
           stage = 0;
           phase ^= 1;
@@ -672,12 +705,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     bool ok = true, first = true;
     for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1, g.err, kErrTimeoutMma, abort_flag)) break;
-      if (!first) {  // the previous tile's share of the common columns has been read
+      if (!first && shared_cols) {  // the previous tile's share of the common columns has been read
         if (!mbar_wait(overlap, ov_phase, g.err, kErrTimeoutMma, abort_flag)) break;
         ov_phase ^= 1;
       }
       first = false;
-      const uint32_t d = tm + (acc ? kAcc1 : 0);
+      const uint32_t d = tm + (acc ? acc1 : 0);
       for (int kt = 0; kt < ki; ++kt) {
         if (!mbar_wait(&full[stage], phase, g.err, kErrTimeoutMma, abort_flag)) {
           ok = false;
@@ -700,8 +733,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int t = 0; t < kTpc; ++t) {
               tc_cp_scales_pair(sc + t * 4, ss + (ch * kTpc + t) * 512);
-              tc_cp_scales_pair(sc + kTpc * 4 + t * 8, ss + (kTps + ch * kTpc + t) * 512);
-              tc_cp_scales_pair(sc + kTpc * 4 + t * 8 + 4, ss + (2 * kTps + ch * kTpc + t) * 512);
+              tc_cp_scales_pair(sc + kTpc * 4 + t * sb * 4, ss + (kTps + ch * kTpc + t) * 512);
+              if (sb == 2)
+                tc_cp_scales_pair(sc + kTpc * 4 + t * 8 + 4, ss + (2 * kTps + ch * kTpc + t) * 512);
             }
 #pragma unroll
             for (int j = 0; j < kStepsPerChunk; ++j) {
@@ -709,8 +743,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               if (k < steps) {
                 const int t = FMT == kMxfp4 ? j >> 1 : j;
                 const uint32_t id = FMT == kMxfp4 ? (uint32_t)(j & 1) * 2 : 0u;
-                tc_mma_mx4<FMT, 2>(d, aa + 2 * k, ba + 2 * k, idesc_mx4<FMT>(256, 256, id),
-                                   sc + t * 4, sc + kTpc * 4 + t * 8, k > 0 ? 1u : (uint32_t)kt);
+                tc_mma_mx4<FMT, 2>(d, aa + 2 * k, ba + 2 * k, idesc_mx4<FMT>(256, bn, id), sc + t * 4,
+                                   sc + kTpc * 4 + t * 4 * sb, k > 0 ? 1u : (uint32_t)kt);
               }
             }
             tc_commit_pair(&slot_free[slot]);
@@ -756,30 +790,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int nt = tile_n(tile);
       if (!mbar_wait(&tfull[acc], acc_phase, g.err, kErrTimeoutEpilogue, abort_flag)) break;
       tc_fence_after();
-      const uint32_t t0 = tmem + (acc ? kAcc1 : 0) + ((uint32_t)(ew * 32) << 16);
+      const uint32_t t0 = tmem + (acc ? acc1 : 0) + ((uint32_t)(ew * 32) << 16);
       if constexpr (!GATED) {
-        // Four 32-column chunks per warp; the first lies in the columns common to both
-        // accumulators (6, 7 of the first, 0, 1 of the second). All are read into registers before
-        // any is stored.
+        // Up to four 32-column chunks per warp, all read into registers before any is stored. Where
+        // the accumulators overlap, the first one lies in the common columns (6, 7 of the first
+        // accumulator, 0, 1 of the second) and frees them.
         uint32_t r[4][32];
+        const int half = (bn / 32 + 1) / 2, count = set ? bn / 32 - half : half;
         auto chunk = [&](int i) {
+          if (!shared_cols) return set * half + i;
           return acc ? (i == 0 ? set : 1 + 3 * set + i) : (i == 0 ? 6 + set : 3 * set + i - 1);
         };
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          tmem_ld_32x32b_x32_nw(t0 + chunk(i) * 32, r[i]);
-          if (i == 0 || i == 3) {
+          if (i < count) tmem_ld_32x32b_x32_nw(t0 + chunk(i) * 32, r[i]);
+          if ((i == 0 && shared_cols) || i == 3) {
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(i == 0 ? overlap0 : tempty0 + acc * 8);
+            if (lane == 0) arrive_relaxed(i == 0 ? overlap0 : tempty0 + acc * 8);
           }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           reg_fence(r[i]);
-          const int col0 = nt * 256 + chunk(i) * 32;
-          if (col0 < g.N && row0 < g.M) {
+          const int col0 = nt * bn + chunk(i) * 32;
+          if (i < count && col0 < g.N && row0 < g.M) {
             float v[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[i][k]) * f;
@@ -802,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tmem_ld_32x32b_x32(t0 + 128 + c * 32, w);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(i == 0 ? overlap0 : tempty0 + acc * 8);
+          if (lane == 0) arrive_relaxed(i == 0 ? overlap0 : tempty0 + acc * 8);
           const int col0 = nt * 128 + c * 32;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -946,6 +982,14 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, tp, tp2, tq, a);
 }
 
+// Columns of a pair's tile. A tile of 128 columns takes 0.8 of the time of one of 256 (6.1 us and
+// 7.7 us at K = 4096), so it pays only where all of them run at once and 256 would leave pairs
+// idle: 512 x 4096 x 4096 10.8 us against 12.4 us.
+int pick_bn(const Mx4Gemm& g, int num_sms) {
+  const long long tiles = (long long)((g.M + 255) / 256) * ((g.N + 127) / 128);
+  return tiles <= num_sms / 2 ? 128 : 256;
+}
+
 template <int FMT, bool GATED>
 cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   using C = PairCfg<FMT>;
@@ -953,8 +997,9 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   const int up0 = (g.N + 127) & ~127;
   CUtensorMap ta, tb, tb2, tsa, tsb;
   const int b_rows = GATED ? 2 * up0 : g.N;
+  const int bn = GATED ? 256 : pick_bn(g, num_sms);
   if (!map_codes(&ta, g.A.codes, g.M, kp, g.A.ld, 128) ||
-      !map_codes(&tb, g.B.codes, g.N, kp, g.B.ld, 128) ||
+      !map_codes(&tb, g.B.codes, g.N, kp, g.B.ld, bn / 2) ||
       !map_codes(&tb2, g.B.codes + (GATED ? up0 * g.B.ld / 2 : 0), g.N, kp, g.B.ld, 128) ||
       !make_tensor_map_tiles(&tsa, g.A.scales, kp / Mx4Fmt<FMT>::kTileCols, (g.M + 127) / 128,
                              g.A.ld / Mx4Fmt<FMT>::kTileCols, C::kTps) ||
@@ -964,7 +1009,8 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   PairArgs a = {};
   a.M = g.M; a.N = g.N; a.kp = kp;
   a.num_m = (g.M + 255) / 256;
-  a.num_n = GATED ? up0 / 128 : (g.N + 255) / 256;
+  a.num_n = GATED ? up0 / 128 : (g.N + bn - 1) / bn;
+  a.bn = bn;
   a.m_fast = g.M <= b_rows;  // the operand that every wave sweeps again is the smaller one
   a.a_factor = g.a_factor; a.b_factor = g.b_factor;
   a.C = g.C; a.c_f32 = g.c_f32; a.ldc = g.ldc;

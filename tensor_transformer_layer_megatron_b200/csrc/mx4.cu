@@ -403,6 +403,7 @@ template <int FMT, typename T, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kTileThreads)
     mx4_quantize_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
                         const float* __restrict__ factor, Mx4Out out, Mx4Out out_t) {
+  launch_dependents();
   grid_dependency_wait();
   const Patch p = Patch::of<8>(cols);
   if (!COLS && p.r - (threadIdx.x & 24) >= rows) return;  // the whole warp is behind the last row

@@ -21,6 +21,15 @@ namespace mgt {
 constexpr int kMxfp4 = 0;
 constexpr int kNvfp4 = 1;
 
+// Let the next kernel of the stream, where it was launched programmatically, start as soon as every
+// CTA of this one has come here. It still waits for this kernel's results (grid_dependency_wait);
+// what it does before is its set-up, and in the products with few rows the fetch of weights into
+// L2. Each kernel that calls this waits for its own predecessor, so results stay ordered along the
+// stream.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <int FMT>
 struct Mx4Fmt {
   static constexpr int kBlock = FMT == kMxfp4 ? 32 : 16;  // elements that share a scale
