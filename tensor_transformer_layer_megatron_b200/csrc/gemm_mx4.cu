@@ -852,9 +852,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
           gate_all(v, g.act);
+          // Columns behind the last are zeros, and so are rows (whose scales may be anything: as
+          // they come they would take the slow path of mx4_codes8).
+          const int live = row < g.M ? g.N - col0 : 0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            v[k] = col0 + k < g.N ? v[k] * w[k] : 0.f;  // columns behind the last are zeros
+          for (int k = 0; k < 32; ++k) v[k] = k < live ? v[k] * w[k] : 0.f;
           constexpr int B = Mx4Fmt<FMT>::kBlock;
           uint32_t codes[4], bytes = 0;
 #pragma unroll
@@ -915,26 +917,25 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   constexpr int NM = GATED ? 2 : 1;
   constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;
   const int most = GATED ? 128 : 256;
-  int bnq = 16;
-  while (bnq < g.M && bnq < most) bnq *= 2;
+  const int bnq = g.M < most ? (g.M + 15) & ~15 : most;
   const int groups = bnq > 128 ? 2 : 1;
   const int kp = (g.K + 127) & ~127, ki = (kp + kStageK - 1) / kStageK;
-  const int tiles = ((g.N + kPRows - 1) / kPRows) * ((g.M + bnq - 1) / bnq);
-  int split = 1;
-  while (split < 8 && split * 2 <= ki && tiles * split * 2 <= 2 * num_sms) split *= 2;
-
   const int stage_bytes = NM * kPBytes + bnq * 128 + (NM + groups) * kTps * 512;
   const int acc = NM * ((bnq + 31) & ~31);
   const int sf_cols = (NM + groups) * kTps * 4;
-  const int room = 227 * 1024 - 2048;
-  const int half = 113 * 1024 - 2048;
-  int stages = half / stage_bytes;  // two CTAs per SM where three stages fit
-  if (stages < 3 || acc + 3 * sf_cols > 256) {
-    stages = room / stage_bytes;
-    while (acc + stages * sf_cols > 512) --stages;
-  } else {
-    while (acc + stages * sf_cols > 256) --stages;
-  }
+  // Stages: two CTAs per SM where each gets two at least, and as many as shared and tensor memory
+  // hold. The partial tile, which takes the stages' place, has to fit into their operands.
+  const int operand_bytes = NM * kPBytes + bnq * 128;
+  auto stages_in = [&](int bytes, int columns) {
+    int n = bytes / stage_bytes;
+    while (n > 0 && acc + n * sf_cols > columns) --n;
+    return n >= 2 && NM * bnq * kPRows * 4 <= n * operand_bytes ? n : 0;
+  };
+  const int half = 113 * 1024 - 2048, room = 227 * 1024 - 2048;
+  int stages = stages_in(half, 256);
+  const bool two = stages > 0;
+  if (!two) stages = stages_in(room, 512);
+  if (!stages) return cudaErrorInvalidConfiguration;
   int cols = 32;
   while (cols < acc + stages * sf_cols) cols *= 2;
   const size_t smem = 1024 + (size_t)stages * stage_bytes + 16 * stages + 64;
@@ -965,20 +966,28 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   cudaError_t e = limit.allow(kern, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((g.N + kPRows - 1) / kPRows) * split),
-                     (unsigned)((g.M + bnq - 1) / bnq));
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  // The sum is split as far as all clusters still run at once with a tenth of the places to spare:
+  // the next kernel's first CTAs start there and fetch its weights. (12288 weight rows, K = 4096,
+  // one token, with its quantisation: two CTAs a tile 9.2 us, three 14.1; 4096 rows, K = 11008: one
+  // 20.3, four 10.1, eight 9.0.)
+  const int tiles_p = (g.N + kPRows - 1) / kPRows, tiles_q = (g.M + bnq - 1) / bnq;
+  const long long tiles = (long long)tiles_p * tiles_q;
+  const int places = (two ? 2 : 1) * num_sms;
+  int split = ki < 8 ? ki : 8;
+  while (split > 1 && tiles * split * 10 > 9 * places) --split;
+  attr[0].val.clusterDim.x = (unsigned)split;
   cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)(tiles_p * split), (unsigned)tiles_q);
   return cudaLaunchKernelEx(&cfg, kern, tp, tp2, tq, a);
 }
 
@@ -1017,11 +1026,13 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   a.up_tiles = up0 / 128;
   a.act = g.act; a.a = g.a; a.out_factor = g.out_factor;
   a.u = static_cast<__nv_bfloat16*>(g.u); a.ldu = g.ldu;
-  // Bulk tensor stores need 16-byte aligned bases and row strides; u's second half starts at
-  // column N.
+  // Bulk tensor stores need 16-byte aligned bases and row strides, and rows that end on 16 bytes:
+  // they write whole 16-byte units (seen with 129 fp32 columns in rows of 132). u's second half
+  // starts at column N.
   CUtensorMap to = {}, to2 = {};
   auto out_map = [&](CUtensorMap* m, void* p, long long ld, int esz) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0 &&
+           ((long long)g.N * esz) % 16 == 0 &&
            make_tensor_map_out_2d(m, p, (uint64_t)g.N, (uint64_t)g.M, (uint64_t)ld, esz == 4);
   };
   if (GATED)
@@ -1039,9 +1050,20 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
                        tb2, tsa, tsb, to, to2, a);
 }
 
+// Rows up to which the weights-as-rows kernel is the faster one (times with the quantisation of the
+// rows, mxfp4). It passes over the weights once per 128 or 256 rows and splits the sum; the pairs'
+// tiles hold 256 rows. N x K = 12288 x 4096: 96 rows 15.0 us against 15.3, 128 rows 16.4 against
+// 15.4; gated 11008 x 4096: 64 rows 18.9 against 22.3, 96 rows 25.8 against 22.5. Where the sum is
+// long and the pairs' tiles leave most SMs idle the split wins further up: 4096 x 11008, 128 rows
+// 16.9 against 22.2, 256 rows 21.2 against 22.7.
+int few_rows(const Mx4Gemm& g, int num_sms) {
+  if (g.gated) return 64;
+  return (g.N + 127) / 128 <= num_sms / 4 && g.K > 8192 ? 256 : 96;
+}
+
 template <int FMT, bool GATED>
 cudaError_t launch_any(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
-  if (g.M > 256) return launch_pair<FMT, GATED>(g, num_sms, s);
+  if (g.M > few_rows(g, num_sms)) return launch_pair<FMT, GATED>(g, num_sms, s);
   return launch_skinny<FMT, GATED>(g, num_sms, s);
 }
 

@@ -93,17 +93,29 @@ class Mx4:
         return self.part(row, rows, 0, self.cols)
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_functions = {}
+
+
 def _matrix(t, name):
-    """(dtype code, row stride) of a 2-D fp32 or bf16 tensor with contiguous rows."""
+    """(dtype code, row stride, rows, columns) of a 2-D fp32 or bf16 tensor with contiguous rows."""
     dtype = t.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if dtype is _BF16:
+        code = 1
+    elif dtype is _F32:
+        code = 0
+    else:
         raise TypeError("%s must be float32 or bfloat16" % name)
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise TypeError("%s must be 2-D with contiguous rows" % name)
-    (rows, cols), (ld, step) = t.shape, t.stride()
+    rows, cols = shape
+    ld, step = t.stride()
     if step != 1 and cols > 1:
         raise TypeError("%s must be 2-D with contiguous rows" % name)
-    return (1 if dtype is torch.bfloat16 else 0), (ld if rows > 1 else max(ld, cols))
+    return code, (ld if rows > 1 else max(ld, cols)), rows, cols
 
 
 def _call(name, device, stream, others, *args):
@@ -113,14 +125,17 @@ def _call(name, device, stream, others, *args):
             raise ValueError("all tensors must be on one device")
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
+    index = device.index
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = _current_stream(index)
     elif stream.device != device:
         raise ValueError("the stream belongs to another device than the tensors")
     else:
         handle = stream.cuda_stream
-    f = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(load_library(), name)
+    if _current_device() == index:
         code = f(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -130,7 +145,7 @@ def _call(name, device, stream, others, *args):
 
 
 def _check_status(status):
-    if status.dtype is not torch.int32:
+    if status.dtype is not _I32:
         raise TypeError("status must be an int32 device word")
 
 
@@ -140,19 +155,19 @@ def _addr(q):
 
 def mx4_tensor_factor(x, factor, stream=None):
     """factor = {amax, f} of a 2-D tensor for "nvfp4" (see mgt_mx4_tensor_factor)."""
-    code, ld = _matrix(x, "x")
+    code, ld, rows, cols = _matrix(x, "x")
     if factor.dtype != torch.float32 or factor.numel() < 2 or not factor.is_contiguous():
         raise TypeError("factor must be two contiguous float32")
-    _call("mgt_mx4_tensor_factor", x.device, stream, (factor,), code, x.shape[0], x.shape[1],
+    _call("mgt_mx4_tensor_factor", x.device, stream, (factor,), code, rows, cols,
           x.data_ptr(), ld, factor.data_ptr())
 
 
 def mx4_quantize(x, q=None, qt=None, stream=None):
     """Quantise x [rows, cols] (fp32 or bf16) into q and / or, transposed, into qt (see
     mgt_mx4_quantize)."""
-    code, ld = _matrix(x, "x")
-    if (q is not None and (q.rows, q.cols) != tuple(x.shape)) or \
-            (qt is not None and (qt.cols, qt.rows) != tuple(x.shape)):
+    code, ld, rows, cols = _matrix(x, "x")
+    if (q is not None and (q.rows != rows or q.cols != cols)) or \
+            (qt is not None and (qt.cols != rows or qt.rows != cols)):
         raise ValueError("q takes x's shape and qt the transposed one")
     _call("mgt_mx4_quantize", x.device, stream, (q, qt), code, x.data_ptr(), ld, _addr(q),
           _addr(qt))
@@ -160,8 +175,8 @@ def mx4_quantize(x, q=None, qt=None, stream=None):
 
 def mx4_dequantize(q, y, stream=None):
     """y [rows, cols] (fp32 or bf16) = what q stands for (see mgt_mx4_dequantize)."""
-    code, ld = _matrix(y, "y")
-    if tuple(y.shape) != (q.rows, q.cols):
+    code, ld, rows, cols = _matrix(y, "y")
+    if rows != q.rows or cols != q.cols:
         raise ValueError("y takes q's shape")
     _call("mgt_mx4_dequantize", y.device, stream, (q,), _addr(q), code, y.data_ptr(), ld)
 
@@ -169,9 +184,9 @@ def mx4_dequantize(q, y, stream=None):
 def gemm_mx4(A, B, C, status, stream=None):
     """C [A.rows, B.rows] (fp32 or bf16) = A B^T of two 4-bit operands (see mgt_gemm_mx4);
     status an int32 device tensor that receives timeout codes."""
-    code, ld = _matrix(C, "C")
+    code, ld, rows, cols = _matrix(C, "C")
     _check_status(status)
-    if tuple(C.shape) != (A.rows, B.rows) or A.cols != B.cols:
+    if rows != A.rows or cols != B.rows or A.cols != B.cols:
         raise ValueError("C must be [A.rows, B.rows], and A and B have the same columns")
     _call("mgt_gemm_mx4", C.device, stream, (A, B, status), _addr(A), _addr(B), C.data_ptr(), code,
           ld, status.data_ptr())

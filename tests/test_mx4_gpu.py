@@ -146,9 +146,9 @@ def product_bound(a, b, bf16, ref):
     return t + (np.abs(ref) * 2.0 ** -8 if bf16 else 0) + 1e-37
 
 
-SHAPES = [(1, 1, 1), (1, 8, 16), (2, 130, 33), (1, 4096, 1024), (7, 257, 4096), (16, 128, 128),
+SHAPES = [(1, 1, 1), (1, 8, 16), (24, 200, 1500), (49, 384, 700), (144, 260, 512), (200, 128, 900), (2, 130, 33), (1, 4096, 1024), (7, 257, 4096), (16, 128, 128),
           (17, 100, 300), (64, 513, 640), (100, 384, 2000), (128, 128, 256), (129, 129, 144),
-          (250, 1000, 777), (300, 520, 4096), (512, 256, 512), (777, 1111, 999), (1500, 640, 384)]
+          (250, 1000, 777), (300, 520, 4096), (512, 256, 512), (777, 1111, 999), (1500, 640, 384), (300, 257, 256)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -160,7 +160,7 @@ def test_product(M, N, K, fmt, out):
     A, B = operand(fmt, M, K, x.cuda(), fx, 0xFF), operand(fmt, N, K, w.cuda(), fw, 0xFF)
     a, b = mx4.values(np64(x), fmt, fx), mx4.values(np64(w), fmt, fw)
     ref = a @ b.T
-    for pad in (0, 3, 8):
+    for pad in (0, 3, 8, 16 - N % 16):  # the last: aligned rows, whose end may not be
         C = torch.full((M + 1, N + pad), 77.0, dtype=TYPES[out], device="cuda")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
         mgt.gemm_mx4(A, B, C[:M, :N], st)
@@ -234,7 +234,8 @@ def gated_weights(fmt, F, K, f, seed):
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M,F,K", [(1, 1, 16), (1, 300, 512), (5, 128, 100), (33, 257, 640), (128, 64, 256),
+@pytest.mark.parametrize("M,F,K", [(1, 1, 16), (1, 300, 512), (5, 128, 100), (33, 257, 640), (90, 130, 600), (96, 260, 512),
+                                   (112, 128, 1024), (128, 64, 256),
                                    (200, 500, 333), (300, 1300, 512), (700, 384, 128)])
 def test_gated_product(M, F, K, fmt, act):
     x = randn(M, K, seed=M)
