@@ -27,6 +27,21 @@ struct Vec8<__nv_bfloat16> {
     }
     a = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // Rows of any alignment: the aligned words that hold the elements; one that starts at an odd
+  // element takes a word more and is put together from neighbours. (Such a word holds an element
+  // of its neighbours too, never anything but.)
+  __device__ __forceinline__ void load_words(const __nv_bfloat16* p) {
+    const uint32_t* w =
+        reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+    a = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+    if (reinterpret_cast<uintptr_t>(p) & 2) {
+      const uint32_t e = __ldg(w + 4);
+      a.x = __byte_perm(a.x, a.y, 0x5432);
+      a.y = __byte_perm(a.y, a.z, 0x5432);
+      a.z = __byte_perm(a.z, a.w, 0x5432);
+      a.w = __byte_perm(a.w, e, 0x5432);
+    }
+  }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
   // Largest |x| as fp32 bits: bf16 magnitudes order like their bits, two to a word.
   __device__ __forceinline__ uint32_t amax() const {
@@ -49,6 +64,10 @@ struct Vec8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_words(const float* p) {
+    a = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    b = make_float4(__ldg(p + 4), __ldg(p + 5), __ldg(p + 6), __ldg(p + 7));
   }
   __device__ __forceinline__ void load_n(const float* p, int n) {
     float v[8];
@@ -77,6 +96,8 @@ __device__ __forceinline__ void load8(Vec8<T>& r, const T* row, int c, int cols,
     r.zero();
   else if (vec && c + 8 <= cols)
     r.load(row + c);
+  else if (c + 8 < cols)
+    r.load_words(row + c);
   else
     r.load_n(row + c, cols - c);
 }
@@ -376,17 +397,15 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
           if (o.first) o.scale[16 * (i + h)] = (uint8_t)s.byte;
         }
       }
-    if constexpr (COLS) {
+  }
+  if constexpr (COLS) {
 #pragma unroll
-      for (int q = 0; q < PC / 2; ++q) {
-        float a0, a1, b0, b1;
-        scaled2<FMT>(x.pair(i, q), cinv[q], cfs[q], a0, a1);
-        scaled2<FMT>(x.pair(i + 1, q), cinv[q], cfs[q], b0, b1);
-        const uint32_t w0 = e2m1x2(a0, b0), w1 = e2m1x2(a1, b1);
-        const uint32_t sel = i == 2 ? 0x3240 : i == 4 ? 0x3410 : 0x4210;
-        cc[2 * q] = i ? prmt(cc[2 * q], w0, sel) : w0;
-        cc[2 * q + 1] = i ? prmt(cc[2 * q + 1], w1, sel) : w1;
-      }
+    for (int q = 0; q < PC / 2; ++q) {
+      float a[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) scaled2<FMT>(x.pair(i, q), cinv[q], cfs[q], a[i], b[i]);
+      cc[2 * q] = e2m1x8(a);
+      cc[2 * q + 1] = e2m1x8(b);
     }
   }
   if constexpr (COLS) {
@@ -432,7 +451,8 @@ __global__ void __launch_bounds__(kTileThreads)
 // From da = dL/da and u = [gate | up]: dg = da * up * act'(gate), dup = da * act(gate), and
 // a = act(gate) * up again. dg and dup leave quantised along the rows (for dX) and along the
 // columns (for dW1), a along the columns (for dW2); none of them is written in 16 bits. Patches of
-// 8 x 4: three results of 32 values stay in registers.
+// 8 x 4: dg is quantised from registers while dup and a wait in shared memory, 16 bytes a lane,
+// each lane its own.
 struct Quad {  // four consecutive bf16
   uint2 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int cols, bool row_ok,
@@ -441,6 +461,14 @@ struct Quad {  // four consecutive bf16
     if (!row_ok || c >= cols) return;
     if (vec && c + 4 <= cols) {
       a = __ldg(reinterpret_cast<const uint2*>(row + c));
+    } else if (c + 4 < cols) {  // the aligned words that hold them (see Vec8)
+      const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+      a = make_uint2(__ldg(w), __ldg(w + 1));
+      if (at & 2) {
+        a.x = prmt(a.x, a.y, 0x5432);
+        a.y = prmt(a.y, __ldg(w + 2), 0x5432);
+      }
     } else {
       uint32_t h[4];
 #pragma unroll
@@ -461,6 +489,7 @@ __global__ void __launch_bounds__(kTileThreads, 4)
                          long long ldu, bool vec_g, bool vec_u, const float* __restrict__ f_du,
                          const float* __restrict__ f_dut, const float* __restrict__ f_at,
                          Mx4Out dg, Mx4Out dup, Mx4Out dgt, Mx4Out dupt, Mx4Out at) {
+  __shared__ float4 kept[2][8][kTileThreads];
   grid_dependency_wait();
   const Patch p = Patch::of<4>(F);
   Quad wd[8], wg[8], wu[8];
@@ -475,33 +504,41 @@ __global__ void __launch_bounds__(kTileThreads, 4)
   const Mx4Factor fc = mx4_factor<FMT>(dgt.codes ? f_dut : nullptr);
   const Mx4Factor fa = mx4_factor<FMT>(at.codes ? f_at : nullptr);
   const int kp = (F + 127) & ~127;
-  // One result at a time: its 32 values and the inputs fit the registers of four CTAs per SM. The
-  // activation is computed again for each, which costs less than holding three results.
   PatchF32<4> v;
-  auto result = [&](auto fn) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // (as if changed, or the compiler keeps the activations after all)
-      asm volatile("" : "+r"(wg[i].a.x));
-      asm volatile("" : "+r"(wg[i].a.y));
+  for (int i = 0; i < 8; ++i) {
+    float b[4], a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float h, dh;
+      gate_and_grad<ACT>(wg[i].at(j), h, dh);
+      const float d = wd[i].at(j), up = wu[i].at(j);
+      v.v[i][j] = d * up * dh;
+      b[j] = d * h;
+      a[j] = h * up;
     }
+    kept[0][i][threadIdx.x] = make_float4(b[0], b[1], b[2], b[3]);
+    kept[1][i][threadIdx.x] = make_float4(a[0], a[1], a[2], a[3]);
+  }
+  asm volatile("" ::: "memory");  // (or the compiler keeps them in registers after all)
+  auto take = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float h, dh;
-        gate_and_grad<ACT>(wg[i].at(j), h, dh);
-        v.v[i][j] = fn(wd[i].at(j), wu[i].at(j), h, dh);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float4 w = kept[k][i][threadIdx.x];
+      v.v[i][0] = w.x;
+      v.v[i][1] = w.y;
+      v.v[i][2] = w.z;
+      v.v[i][3] = w.w;
+    }
   };
   constexpr bool kPacked = FMT == kMxfp4;
   if (dg.codes || dgt.codes) {
-    result([](float d, float up, float, float dh) { return d * up * dh; });
     quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dg, dgt, fr, fc);
-    result([](float d, float, float h, float) { return d * h; });
+    take(0);
     quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dup, dupt, fr, fc);
   }
   if (at.codes) {
-    result([](float, float up, float h, float) { return h * up; });
+    take(1);
     quantize_patch<FMT, kPacked, false, true>(v, p, rows, F, kp, at, at, fa, fa);
   }
 }
