@@ -206,12 +206,12 @@ struct Patch {
 struct PatchOut {
   uint8_t *codes, *scale;
   long long step;
-  bool first;  // this lane writes the block's scale
   template <int FMT>
-  __device__ __forceinline__ static PatchOut of(const Mx4Out& o, long long row, long long col) {
+  __device__ __forceinline__ static PatchOut of(const Mx4Out& o, long long row, long long col,
+                                                long long scale_col) {
     return PatchOut{o.codes + (row * o.ld + col) / 2,
-                    o.scales + mx4_scale_off<FMT>(row, (int)(col / Mx4Fmt<FMT>::kBlock), o.ld),
-                    o.ld / 2, col % Mx4Fmt<FMT>::kBlock == 0};
+                    o.scales + mx4_scale_off<FMT>(row, (int)(scale_col / Mx4Fmt<FMT>::kBlock), o.ld),
+                    o.ld / 2};
   }
 };
 
@@ -321,6 +321,48 @@ __device__ __forceinline__ void scaled2(uint64_t x, uint64_t inv, uint64_t neg_f
   f2_unpack(y, a, b);
 }
 
+// Scale bytes of a warp's 32 rows (b: of this lane's eight rows, in its block): every lane writes one
+// row's bytes, all NB blocks that the warp covers, as one store instead of eight by a few lanes
+// each. Lane c of the eight along a row takes row c of the eight, and the other blocks' bytes of it
+// from their lanes. `scale`: of the patch's first row, the warp's first block.
+template <int NB>
+__device__ __forceinline__ void put_row_scales(const uint32_t (&b)[8], uint8_t* scale, int nrows) {
+  const int c = threadIdx.x & 7;
+  const uint32_t lo = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+  const uint32_t hi = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+  auto byte = [&](int row) { return ((row & 4 ? hi : lo) >> (8 * (row & 3))) & 255u; };
+  const int mine = c / (8 / NB);
+  uint32_t w = byte(c) << (8 * mine);
+#pragma unroll
+  for (int k = 1; k < NB; ++k) {
+    const int x = k * (8 / NB);
+    w |= __shfl_xor_sync(0xffffffffu, byte(c ^ x), x) << (8 * (mine ^ k));
+  }
+  if (c < nrows) {
+    scale += 16 * c;
+    if constexpr (NB == 4)
+      *reinterpret_cast<uint32_t*>(scale) = w;
+    else if constexpr (NB == 2)
+      *reinterpret_cast<uint16_t*>(scale) = (uint16_t)w;
+    else
+      *scale = (uint8_t)w;
+  }
+}
+// Scale bytes of this lane's PC columns (b): the G lanes that share the blocks write PC / G each.
+template <int PC, int G>
+__device__ __forceinline__ void put_col_scales(const uint32_t (&b)[PC], uint8_t* scale, int ncols) {
+  constexpr int kEach = PC / G;
+  const int g = (threadIdx.x >> 3) & (G - 1);
+#pragma unroll
+  for (int m = 0; m < kEach; ++m) {
+    uint32_t v = b[m];
+#pragma unroll
+    for (int k = 1; k < G; ++k) v = g == k ? b[k * kEach + m] : v;
+    const int j = g * kEach + m;
+    if (j < ncols) scale[16 * j] = (uint8_t)v;
+  }
+}
+
 // Quantise a patch along its rows (into `out`) and / or its columns (into `out_t`); an operand
 // without codes is left out.
 template <int FMT, bool PACKED, bool ROWS, bool COLS, typename P>
@@ -358,7 +400,9 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
       ft.inv *= 1.0f / k;
     }
   }
-  const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c), t = PatchOut::of<FMT>(out_t, p.c, p.r);
+  // row scales: of the warp's first block; column scales: of this lane's
+  const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c, p.c - (threadIdx.x & 7) * PC);
+  const PatchOut t = PatchOut::of<FMT>(out_t, p.c, p.r, p.r);
   const bool put_rows = ROWS && out.codes && p.c < kp;
   uint64_t cinv[PC / 2], cfs[PC / 2];
   uint32_t cc[PC], cmask[PC];
@@ -370,11 +414,10 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
       cfs[q] = f2_pack(-a.fs, -b.fs);
       cmask[2 * q] = a.mask;
       cmask[2 * q + 1] = b.mask;
-      if (out_t.codes && t.first) {
-        if (p.c + 2 * q < cols) t.scale[32 * q] = (uint8_t)a.byte;
-        if (p.c + 2 * q + 1 < cols) t.scale[32 * q + 16] = (uint8_t)b.byte;
-      }
+      cm[2 * q] = a.byte;
+      cm[2 * q + 1] = b.byte;
     }
+    put_col_scales<PC, B / 8>(cm, t.scale, out_t.codes ? cols - p.c : 0);
   }
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
@@ -394,9 +437,13 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
           else
             *reinterpret_cast<uint16_t*>(d) =
                 (uint16_t)((e2m1x2(e[0], e[1]) | (e2m1x2(e[2], e[3]) << 8)) & s.mask);
-          if (o.first) o.scale[16 * (i + h)] = (uint8_t)s.byte;
         }
+        rm[i + h] = s.byte;
       }
+  }
+  if constexpr (ROWS) {
+    const long long left = rows - p.r;
+    put_row_scales<8 * PC / B>(rm, o.scale, put_rows && left > 0 ? (int)(left < 8 ? left : 8) : 0);
   }
   if constexpr (COLS) {
 #pragma unroll
