@@ -7,6 +7,8 @@
 // scales inside the sum.
 #include <cudaTypedefs.h>
 
+#include <mutex>
+
 #include "mx4_device.cuh"
 #include "mx4_internal.h"
 
@@ -903,9 +905,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ---------------------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+template <int RANK>
+bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base,
+            const cuuint64_t (&dims)[RANK], const cuuint64_t (&strides)[RANK - 1],
+            const cuuint32_t (&box)[RANK], CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  cuuint32_t es[RANK];
+  for (int i = 0; i < RANK; ++i) es[i] = 1;
+  return fn && fn(m, type, RANK, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Codes of an operand as bytes, boxes of 128 bytes (256 elements) by box_rows rows with the
+// swizzle that the tensor core reads; zeros out of bounds.
 bool map_codes(CUtensorMap* m, const uint8_t* codes, int rows, int kp, long long ld, int box_rows) {
-  return make_tensor_map_u8_2d(m, codes, (uint64_t)kp / 2, (uint64_t)rows, (uint64_t)ld / 2,
-                               (uint32_t)box_rows);
+  return encode<2>(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes,
+                   {(cuuint64_t)kp / 2, (cuuint64_t)rows}, {(cuuint64_t)ld / 2},
+                   {128, (cuuint32_t)box_rows}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scale tiles [rows of tiles][ld tiles], `tiles` of each row inside; boxes of box_tiles tiles.
+bool map_tiles(CUtensorMap* m, const uint8_t* scales, long long tiles, long long rows,
+               long long ld, int box_tiles) {
+  return encode<3>(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales,
+                   {128, (cuuint64_t)tiles, (cuuint64_t)rows}, {512, (cuuint64_t)ld * 512},
+                   {128, (cuuint32_t)box_tiles, 1}, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+// Output, boxes of 32 by 32.
+bool map_out(CUtensorMap* m, void* base, int cols, int rows, long long ld, bool f32) {
+  return encode<2>(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   base, {(cuuint64_t)cols, (cuuint64_t)rows}, {(cuuint64_t)ld * (f32 ? 4 : 2)},
+                   {32, 32}, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool store_vec4(const void* p, long long ld, int esz) {
@@ -1010,9 +1054,9 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   if (!map_codes(&ta, g.A.codes, g.M, kp, g.A.ld, 128) ||
       !map_codes(&tb, g.B.codes, g.N, kp, g.B.ld, bn / 2) ||
       !map_codes(&tb2, g.B.codes + (GATED ? up0 * g.B.ld / 2 : 0), g.N, kp, g.B.ld, 128) ||
-      !make_tensor_map_tiles(&tsa, g.A.scales, kp / Mx4Fmt<FMT>::kTileCols, (g.M + 127) / 128,
+      !map_tiles(&tsa, g.A.scales, kp / Mx4Fmt<FMT>::kTileCols, (g.M + 127) / 128,
                              g.A.ld / Mx4Fmt<FMT>::kTileCols, C::kTps) ||
-      !make_tensor_map_tiles(&tsb, g.B.scales, kp / Mx4Fmt<FMT>::kTileCols, (b_rows + 127) / 128,
+      !map_tiles(&tsb, g.B.scales, kp / Mx4Fmt<FMT>::kTileCols, (b_rows + 127) / 128,
                              g.B.ld / Mx4Fmt<FMT>::kTileCols, C::kTps))
     return cudaErrorInvalidValue;
   PairArgs a = {};
@@ -1033,7 +1077,7 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   auto out_map = [&](CUtensorMap* m, void* p, long long ld, int esz) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0 &&
            ((long long)g.N * esz) % 16 == 0 &&
-           make_tensor_map_out_2d(m, p, (uint64_t)g.N, (uint64_t)g.M, (uint64_t)ld, esz == 4);
+           map_out(m, p, g.N, g.M, ld, esz == 4);
   };
   if (GATED)
     a.tma = a.u && out_map(&to, a.u, g.ldu, 2) && out_map(&to2, a.u + g.N, g.ldu, 2);

@@ -1054,47 +1054,6 @@ bool make_tensor_map_i32_3d(CUtensorMap* m, const void* base, const uint64_t dim
   return r == CUDA_SUCCESS;
 }
 
-bool make_tensor_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
-                           uint64_t ld, uint32_t box_rows) {
-  auto fn = get_encode_fn();
-  if (!fn) return false;
-  cuuint64_t gd[2] = {inner, rows};
-  cuuint64_t gs[1] = {ld};
-  cuuint32_t bd[2] = {128, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gd, gs, bd, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_tensor_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t rows,
-                           uint64_t ld, uint32_t box_tiles) {
-  auto fn = get_encode_fn();
-  if (!fn) return false;
-  cuuint64_t gd[3] = {128, tiles, rows};
-  cuuint64_t gs[2] = {512, ld * 512};
-  cuuint32_t bd[3] = {128, box_tiles, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), gd, gs, bd, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_tensor_map_out_2d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t ld,
-                            bool f32) {
-  auto fn = get_encode_fn();
-  if (!fn) return false;
-  const int esz = f32 ? 4 : 2;
-  cuuint64_t gd[2] = {cols, rows};
-  cuuint64_t gs[1] = {ld * esz};
-  cuuint32_t bd[2] = {32, 32};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
-            gd, gs, bd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 namespace {
 
 bool make_map(CUtensorMap* m, const void* base, const uint64_t dims[3], const uint64_t strides[2],

@@ -131,18 +131,6 @@ bool make_tensor_map_bf16_3d(CUtensorMap* m, const void* base, const uint64_t di
 // 3-D int32 tensor map without swizzle (row-major boxes); strides in elements.
 bool make_tensor_map_i32_3d(CUtensorMap* m, const void* base, const uint64_t dims[3],
                             const uint64_t strides[2], const uint32_t box[3]);
-// 2-D byte tensor map {inner, rows}, row stride ld bytes, box 128 x box_rows (128-byte swizzle,
-// zero fill out of bounds).
-bool make_tensor_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
-                           uint64_t ld, uint32_t box_rows);
-// Tensor map over 512-byte tiles [rows][ld tiles], `tiles` of each row inside; box one row by
-// box_tiles tiles, unswizzled, zero fill out of bounds.
-bool make_tensor_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t rows,
-                           uint64_t ld, uint32_t box_tiles);
-// Output map {cols, rows}, row stride ld elements, box 32 x 32; fp32 with 128-byte, bf16 with
-// 64-byte swizzle.
-bool make_tensor_map_out_2d(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t ld,
-                            bool f32);
 
 // tcgen05 / TMA GEMM for bf16 operands (fp32 accumulate in tensor memory).
 // Builds the tensor maps from the pointers in `args` (A, B, strides) and launches a persistent

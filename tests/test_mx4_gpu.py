@@ -171,6 +171,85 @@ def test_product(M, N, K, fmt, out):
         assert (C[M] == 77).all() and (C[:, N:] == 77).all()
 
 
+def values_of(q):
+    y = torch.empty(q.rows, q.cols, device="cuda")
+    mgt.mx4_dequantize(q, y)
+    return y.double()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_product_of_every_row_count(fmt):
+    """Row counts around every step of the few-row kernel's shapes, with a sum long enough that it
+    keeps up to 256 rows, and around its end; against the dequantised operands in float64."""
+    K, N = 8500, 300
+    f = 2.0 ** -6 if fmt == "nvfp4" else 1.0
+    w = operand(fmt, N, K, randn(N, K, seed=1, scale=0.05).cuda(), f)
+    x = randn(258, K, seed=2).cuda()
+    wv = values_of(w)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    steps = -(-K // 64)
+    for M in (1, 15, 16, 17, 31, 33, 48, 49, 64, 65, 79, 81, 95, 97, 111, 112, 127, 128, 129, 143, 145, 176,
+              177, 191, 193, 208, 209, 223, 225, 239, 241, 255, 256, 257, 258):
+        q = operand(fmt, M, K, x[:M], f, 0xFF)
+        C = torch.full((M, N), float("nan"), device="cuda")
+        mgt.gemm_mx4(q, w, C, st)
+        xv = values_of(q)
+        ref = xv @ wv.t()
+        bound = xv.abs() @ wv.abs().t() * (4 * steps * 2.0 ** -23) + ref.abs() * 2.0 ** -23
+        assert ((C.double() - ref).abs() <= bound).all(), M
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_operands_beyond_32_bit_offsets(fmt):
+    """70001 x 65500 elements: 4.6e9, 2.3 GB of codes. The last rows' bytes are those of the same rows
+    quantised alone, in both layouts, and a product's last rows those of a product of that part."""
+    R, C, t = 70001, 65500, 129
+    x = torch.randn(R, C, dtype=torch.bfloat16, device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    q = operand(fmt, R, C, x)
+    r0 = (R - t) // 128 * 128
+    part, alone = q.rows_view(r0, R - r0), operand(fmt, R - r0, C, x[r0:].contiguous())
+    assert torch.equal(q.codes[r0:], alone.codes)
+    a, b = values_of(part), values_of(alone)
+    assert torch.equal(a, b) and float(a.abs().max()) > 1
+    v = operand(fmt, 33, C, randn(33, C, seed=3).cuda())
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for A, B, rows in ((v, q, None), (q, v, slice(r0, None))):
+        out = torch.empty(A.rows, B.rows, device="cuda")
+        mgt.gemm_mx4(A, B, out, st)
+        small = torch.empty((33, R - r0) if A is v else (R - r0, 33), device="cuda")
+        mgt.gemm_mx4(v if A is v else part, part if A is v else v, small, st)
+        got = out[:, r0:] if A is v else out[rows]
+        ref = values_of(v) @ a.t() if A is v else a @ values_of(v).t()
+        scale = float(ref.abs().max())
+        # 1024 steps of at most 4 units of 2^-23 of the partial sums, which stay below 256 times a
+        # result's largest value (sums of 65500 signed products against their magnitudes')
+        assert float((got.double() - ref).abs().max()) <= 1024 * 4 * 2.0 ** -23 * 256 * scale
+        assert float((small.double() - ref).abs().max()) <= 1024 * 4 * 2.0 ** -23 * 256 * scale
+    del q, part
+    qt = operand(fmt, C, R)
+    mgt.mx4_quantize(x, None, qt)
+    last = operand(fmt, 128, R)
+    mgt.mx4_quantize(x[:, C // 128 * 128 - 128:C // 128 * 128].contiguous(), None, last)
+    c0 = C // 128 * 128 - 128
+    assert torch.equal(qt.codes[c0:c0 + 128], last.codes)
+    assert torch.equal(values_of(qt.rows_view(c0, 128)), values_of(last))
+    assert int(st) == 0
+
+
+def test_quantize_with_a_factor_that_is_no_power_of_two():
+    """A kept scale from elsewhere: x / (f s) is then rounded twice, each by at most 2^-24, so only
+    elements within 2^-22 of a border may go to the other side."""
+    x, f = randn(64, 512, seed=5).cuda(), float(np.float32(0.0137))
+    q = operand("nvfp4", 64, 512, x, f)
+    y = values_of(q).cpu().numpy()
+    lo, hi = (mx4.quantize(np64(x) * (1 + e), "nvfp4", f) for e in (-2.0 ** -22, 2.0 ** -22))
+    sure = (lo[0] == hi[0])[:, :512] & np.repeat(lo[1] == hi[1], 16, 1)[:, :512]
+    assert sure.mean() > 0.999
+    ref = mx4.values(np64(x), "nvfp4", f)
+    assert (np.abs(y - ref)[sure] <= 2.0 ** -22 * np.abs(ref)[sure]).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_product_carries_infinities_and_nans(fmt):
     """A block that cannot be scaled makes the sums that it enters NaN, and no others."""
