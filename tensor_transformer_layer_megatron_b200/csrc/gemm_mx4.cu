@@ -560,10 +560,20 @@ __device__ __forceinline__ void store_block_any(uint8_t* stg, const float (&v)[3
   __syncwarp();
   T* out = base + (long long)row0 * ld + col0;
   const int nr = min(32, rows - row0), nc = min(32, cols - col0);
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const T e = reinterpret_cast<const T*>(stg + r * kRow)[lane];
-    if (r < nr && lane < nc) out[(long long)r * ld + lane] = e;
+  // Eight rows read before the first is written: the compiler does not move a shared load across a
+  // global store, and one round trip per row made this the slowest part of ragged products (2048 x
+  // 12287 x 4096 68 us, now 52, 47 where bulk stores apply).
+  T* o = out + lane;
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    T e[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) e[r] = reinterpret_cast<const T*>(stg + (r0 + r) * kRow)[lane];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (r0 + r < nr && lane < nc) *o = e[r];
+      o += ld;
+    }
   }
   __syncwarp();
 }
@@ -1027,8 +1037,26 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   const int tiles_p = (g.N + kPRows - 1) / kPRows, tiles_q = (g.M + bnq - 1) / bnq;
   const long long tiles = (long long)tiles_p * tiles_q;
   const int places = (two ? 2 : 1) * num_sms;
+  // With one CTA per SM, how many clusters of a size are resident at once depends on how they fill
+  // the GPU's processor groups (16 clusters of eight do not: 4096 x 100 x 4096 took 18.7 us with
+  // them, 11.0 without): the driver is asked, once per size and shape. With two per SM its answer
+  // is lower than what runs best.
+  static std::atomic<int> resident[17][9];  // clusters + 1, by bnq / 16 and size
   int split = ki < 8 ? ki : 8;
-  while (split > 1 && tiles * split * 10 > 9 * places) --split;
+  for (; split > 1; --split) {
+    if (tiles * split * 10 > 9 * places) continue;
+    if (two) break;
+    int n = resident[bnq / 16][split].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cfg.gridDim = dim3((unsigned)split);
+      cfg.numAttrs = 1;
+      attr[0].val.clusterDim.x = (unsigned)split;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      resident[bnq / 16][split].store(++n, std::memory_order_relaxed);
+    }
+    if (tiles < n) break;
+  }
   attr[0].val.clusterDim.x = (unsigned)split;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)(tiles_p * split), (unsigned)tiles_q);
@@ -1094,21 +1122,26 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
                        tb2, tsa, tsb, to, to2, a);
 }
 
-// Rows up to which the weights-as-rows kernel is the faster one (times with the quantisation of the
-// rows, mxfp4). It passes over the weights once per 128 or 256 rows and splits the sum; the pairs'
+// Whether the weights-as-rows kernel is the faster one (times with the quantisation of the rows,
+// mxfp4). It passes over the weights once per 128 or 256 rows and splits the sum; the pairs'
 // tiles hold 256 rows. N x K = 12288 x 4096: 96 rows 15.0 us against 15.3, 128 rows 16.4 against
 // 15.4; gated 11008 x 4096: 64 rows 18.9 against 22.3, 96 rows 25.8 against 22.5. Where the sum is
 // long and the pairs' tiles leave most SMs idle the split wins further up: 4096 x 11008, 128 rows
-// 16.9 against 22.2, 256 rows 21.2 against 22.7.
-int few_rows(const Mx4Gemm& g, int num_sms) {
-  if (g.gated) return 64;
-  return (g.N + 127) / 128 <= num_sms / 4 && g.K > 8192 ? 256 : 96;
+// 16.9 against 22.2, 256 rows 21.2 against 22.7; and with six CTAs or more to a tile at any number
+// of rows: 512 x 512 x 8192 10.3 against 15.2, 1000 x 128 x 16384 11.6 against 25.6 (products alone).
+bool few_rows(const Mx4Gemm& g, int num_sms) {
+  if (g.gated) return g.M <= 64;
+  if (g.M <= 96) return true;
+  const long long tiles = (long long)((g.M + 255) / 256) * ((g.N + 127) / 128);
+  const int ki = (g.K + kStageK - 1) / kStageK;
+  return (tiles * 6 * 10 <= 9 * num_sms && ki >= 20) ||
+         (g.M <= 256 && tiles <= num_sms / 4 && ki > 32);
 }
 
 template <int FMT, bool GATED>
 cudaError_t launch_any(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
-  if (g.M > few_rows(g, num_sms)) return launch_pair<FMT, GATED>(g, num_sms, s);
-  return launch_skinny<FMT, GATED>(g, num_sms, s);
+  if (few_rows(g, num_sms)) return launch_skinny<FMT, GATED>(g, num_sms, s);
+  return launch_pair<FMT, GATED>(g, num_sms, s);
 }
 
 }  // namespace
