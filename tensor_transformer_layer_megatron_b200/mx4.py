@@ -62,6 +62,7 @@ class Mx4:
                   raise ValueError("codes, scales and factor must be on one device")
         self.fmt, self.rows, self.cols = fmt, rows, cols
         self.codes, self.scales, self.factor, self.device = codes, scales, factor, codes.device
+        self.index = codes.get_device()
         self._bind(0, 0)
 
     def _bind(self, row, col):
@@ -84,7 +85,7 @@ class Mx4:
         p = object.__new__(Mx4)
         p.fmt, p.rows, p.cols, p.ld = self.fmt, int(rows), int(cols), self.ld
         p.codes, p.scales, p.factor = self.codes, self.scales, self.factor
-        p.device = self.device
+        p.device, p.index = self.device, self.index
         p._bind(self._row + row, self._col + col)
         return p
 
@@ -118,17 +119,26 @@ def _matrix(t, name):
     return code, (ld if rows > 1 else max(ld, cols)), rows, cols
 
 
-def _call(name, device, stream, others, *args):
-    """Launch on `device` (all tensors' device), on its current stream unless one is given."""
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors must be on one device")
-    if device.type != "cuda":
+def _index(*things):
+    """The CUDA device index that all tensors and operands (or None) share."""
+    index = None
+    for t in things:
+        if t is not None:
+            i = t.index if type(t) is Mx4 else t.get_device()
+            if index is None:
+                index = i
+            elif i != index:
+                raise ValueError("all tensors must be on one device")
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    index = device.index
+    return index
+
+
+def _call(name, index, stream, *args):
+    """Launch on device `index`, on its current stream unless one is given."""
     if stream is None:
         handle = _current_stream(index)
-    elif stream.device != device:
+    elif stream.device.index != index:
         raise ValueError("the stream belongs to another device than the tensors")
     else:
         handle = stream.cuda_stream
@@ -138,7 +148,7 @@ def _call(name, device, stream, others, *args):
     if _current_device() == index:
         code = f(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = f(*args, handle)
     if code:
         _check(code, name)
@@ -158,7 +168,7 @@ def mx4_tensor_factor(x, factor, stream=None):
     code, ld, rows, cols = _matrix(x, "x")
     if factor.dtype != torch.float32 or factor.numel() < 2 or not factor.is_contiguous():
         raise TypeError("factor must be two contiguous float32")
-    _call("mgt_mx4_tensor_factor", x.device, stream, (factor,), code, rows, cols,
+    _call("mgt_mx4_tensor_factor", _index(x, factor), stream, code, rows, cols,
           x.data_ptr(), ld, factor.data_ptr())
 
 
@@ -169,7 +179,7 @@ def mx4_quantize(x, q=None, qt=None, stream=None):
     if (q is not None and (q.rows != rows or q.cols != cols)) or \
             (qt is not None and (qt.cols != rows or qt.rows != cols)):
         raise ValueError("q takes x's shape and qt the transposed one")
-    _call("mgt_mx4_quantize", x.device, stream, (q, qt), code, x.data_ptr(), ld, _addr(q),
+    _call("mgt_mx4_quantize", _index(x, q, qt), stream, code, x.data_ptr(), ld, _addr(q),
           _addr(qt))
 
 
@@ -178,7 +188,7 @@ def mx4_dequantize(q, y, stream=None):
     code, ld, rows, cols = _matrix(y, "y")
     if rows != q.rows or cols != q.cols:
         raise ValueError("y takes q's shape")
-    _call("mgt_mx4_dequantize", y.device, stream, (q,), _addr(q), code, y.data_ptr(), ld)
+    _call("mgt_mx4_dequantize", _index(y, q), stream, _addr(q), code, y.data_ptr(), ld)
 
 
 def gemm_mx4(A, B, C, status, stream=None):
@@ -188,8 +198,8 @@ def gemm_mx4(A, B, C, status, stream=None):
     _check_status(status)
     if rows != A.rows or cols != B.rows or A.cols != B.cols:
         raise ValueError("C must be [A.rows, B.rows], and A and B have the same columns")
-    _call("mgt_gemm_mx4", C.device, stream, (A, B, status), _addr(A), _addr(B), C.data_ptr(), code,
-          ld, status.data_ptr())
+    _call("mgt_gemm_mx4", _index(C, A, B, status), stream, A._addr, B._addr, C.data_ptr(), code, ld,
+          status.data_ptr())
 
 
 def gemm_mx4_gated(X, W, a, status, act="silu", u=None, stream=None):
@@ -206,8 +216,8 @@ def gemm_mx4_gated(X, W, a, status, act="silu", u=None, stream=None):
             raise ValueError("u must be [X.rows, 2 * a.cols]")
     if act not in ACTIVATIONS:
         raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
-    _call("mgt_gemm_mx4_gated", a.device, stream, (X, W, u, status), _addr(X), _addr(W),
-          ACTIVATIONS[act], _addr(a), None if u is None else u.data_ptr(), ldu,
+    _call("mgt_gemm_mx4_gated", _index(a, X, W, u, status), stream, X._addr, W._addr,
+          ACTIVATIONS[act], a._addr, None if u is None else u.data_ptr(), ldu,
           status.data_ptr())
 
 
@@ -222,6 +232,6 @@ def mx4_gated_bwd(da, u, du=None, dut=None, at=None, act="silu", stream=None):
         raise ValueError("u must be [rows, 2 * ffn]")
     if act not in ACTIVATIONS:
         raise ValueError("act must be one of %s" % sorted(ACTIVATIONS))
-    _call("mgt_mx4_gated_bwd", da.device, stream, (u, du, dut, at), ACTIVATIONS[act],
+    _call("mgt_mx4_gated_bwd", _index(da, u, du, dut, at), stream, ACTIVATIONS[act],
           da.shape[0], da.shape[1], da.data_ptr(), ldda, u.data_ptr(), ldu,
           _addr(du), _addr(dut), _addr(at))
