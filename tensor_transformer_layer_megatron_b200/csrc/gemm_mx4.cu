@@ -117,6 +117,11 @@ constexpr int kPrefetchStages = 8;    // stages fetched into L2 ahead: 128 KB a 
 // summed axis is split over a cluster of up to eight CTAs, whose fp32 partial tiles meet in
 // distributed shared memory, added in rank order. Gated: two accumulators, gate and up rows of
 // the same outputs.
+//
+// Bound by the weights' bytes and, at these sizes, by what comes before and after them (launch,
+// first loads, sum over the cluster): one token, mxfp4, 12288 x 4096 7.8 us with its launch (26.7
+// MB, 3.4 TB/s), 4096 x 11008 7.6 us, 49152 x 4096 28 us; gated 2 x 11008 x 4096 11.1 us (nvfp4
+// 13.1).
 struct SkinnyArgs {
   int M, N, kp;                 // tokens, weight rows (per matrix), K rounded up to 128
   int bnq, stages, tmem_cols;
@@ -435,6 +440,11 @@ __global__ void __launch_bounds__(192)
 // once the products that read it have completed.
 //
 // Gated: B is 128 gate rows (CTA 0) and the 128 up rows of the same outputs (CTA 1).
+//
+// Bound by the tensor core and the shared memory that feeds it: a stage of 256 elements takes 650
+// to 710 cycles where its products alone take 512, and the hand-over between tiles about 1,500. 8192
+// x 24576 x 6144 mxfp4 457 us (5.4 PFLOP/s), nvfp4 500; 2048 x 12288 x 4096 57 / 62 us, 12288 x 4096
+// x 2048 into fp32 66; gated 2048 x 2 * 11008 x 4096 74 / 80 us, with u kept 83 / 90.
 struct PairArgs {
   int M, N, kp;
   int num_m, num_n, m_fast;
@@ -562,7 +572,7 @@ __device__ __forceinline__ void store_block_any(uint8_t* stg, const float (&v)[3
   const int nr = min(32, rows - row0), nc = min(32, cols - col0);
   // Eight rows read before the first is written: the compiler does not move a shared load across a
   // global store, and one round trip per row made this the slowest part of ragged products (2048 x
-  // 12287 x 4096 68 us, now 52, 47 where bulk stores apply).
+  // 12287 x 4096 68 us row by row, 52 in eights; 47 for 12288, where bulk stores apply).
   T* o = out + lane;
 #pragma unroll
   for (int r0 = 0; r0 < 32; r0 += 8) {

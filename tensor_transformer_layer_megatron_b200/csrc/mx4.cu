@@ -9,13 +9,39 @@
 namespace mgt {
 namespace {
 
+// Plain global loads, in program order with grid_dependency_wait(): the kernel before may still be
+// writing these bytes while this one is already resident, so they are not read-only for its life
+// and take neither the read-only path nor a place ahead of the wait.
+__device__ __forceinline__ uint32_t ld4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 as_float4(uint4 w) {
+  return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                     __uint_as_float(w.w));
+}
+
 template <typename T>
 struct Vec8;  // eight consecutive elements as loaded
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    a = __ldg(reinterpret_cast<const uint4*>(p));
+    a = ld16(p);
   }
   __device__ __forceinline__ void load_n(const __nv_bfloat16* p, int n) {
     uint32_t w[4];
@@ -33,9 +59,9 @@ struct Vec8<__nv_bfloat16> {
   __device__ __forceinline__ void load_words(const __nv_bfloat16* p) {
     const uint32_t* w =
         reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-    a = make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+    a = make_uint4(ld4(w), ld4(w + 1), ld4(w + 2), ld4(w + 3));
     if (reinterpret_cast<uintptr_t>(p) & 2) {
-      const uint32_t e = __ldg(w + 4);
+      const uint32_t e = ld4(w + 4);
       a.x = __byte_perm(a.x, a.y, 0x5432);
       a.y = __byte_perm(a.y, a.z, 0x5432);
       a.z = __byte_perm(a.z, a.w, 0x5432);
@@ -62,12 +88,12 @@ template <>
 struct Vec8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = as_float4(ld16(p));
+    b = as_float4(ld16(p + 4));
   }
   __device__ __forceinline__ void load_words(const float* p) {
-    a = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
-    b = make_float4(__ldg(p + 4), __ldg(p + 5), __ldg(p + 6), __ldg(p + 7));
+    a = as_float4(make_uint4(ld4(p), ld4(p + 1), ld4(p + 2), ld4(p + 3)));
+    b = as_float4(make_uint4(ld4(p + 4), ld4(p + 5), ld4(p + 6), ld4(p + 7)));
   }
   __device__ __forceinline__ void load_n(const float* p, int n) {
     float v[8];
@@ -128,11 +154,22 @@ struct Walk {
 // out = {amax over the finite elements, f = 2^ceil(log2(amax / 2688)), 1 for amax = 0}: 2688 =
 // 6 * 448 is the largest product of an element and a block scale. Block maxima meet in an
 // atomic maximum on the bits of out[0] (order free); the last block to arrive, counted in
-// out[1], writes f over the count. Both words are zeroed before the launch.
+// out[1], writes f over the count. Both words are zeroed by a launch before, of one thread:
+// chained programmatically the two take 2.9 us for one row, with a memory set in its place 6.2.
+// Bound by HBM: 4096 x 11008 fp32 29 us (6.2 TB/s), 2048 x 4096 bf16 6.4 us. 256 threads with
+// four loads in flight, up to eight blocks per SM: no other shape tried was faster anywhere.
+__global__ void mx4_zero2_kernel(float* out) {
+  launch_dependents();
+  grid_dependency_wait();
+  out[0] = out[1] = 0.f;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, const T* __restrict__ x,
+__global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, const T* x,
                                                          long long ldx, bool vec, float* out) {
   __shared__ uint32_t red[8];
+  launch_dependents();
+  grid_dependency_wait();
   uint32_t m = 0;
   constexpr int U = 4;
   Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, (cols + 7) / 8);
@@ -185,6 +222,12 @@ __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, con
 // rows and along its columns, and the largest magnitude of a block is a shuffle over the two or
 // four (gated: four or eight) lanes that share it, along either direction: the transposed operand
 // needs no trip through shared memory, and a lane has eight loads in flight.
+//
+// Times (mxfp4 / nvfp4): bf16 along the rows 2048 x 4096 6.4 / 8.6 us, 8192 x 6144 26 / 34 us
+// (4.8 TB/s / 3.7); bf16 both ways 2048 x 12288 22 / 27 us; fp32 both ways 4096 x 11008 48 / 49 us
+// (4.8 TB/s). What bounds it is HBM for fp32 and, for bf16 and for nvfp4's quotients, the integer
+// and fp32 instructions per element (both ways: 59 % of the ALU's peak, 2.4 instructions a clock
+// and SM). Rows that do not start on 16 bytes are read by words: 10.0 / 14.2 us for 2048 x 4096.
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 128;
 
@@ -467,8 +510,8 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
 
 template <int FMT, typename T, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kTileThreads)
-    mx4_quantize_kernel(int rows, int cols, const T* __restrict__ x, long long ldx, bool vec,
-                        const float* __restrict__ factor, Mx4Out out, Mx4Out out_t) {
+    mx4_quantize_kernel(int rows, int cols, const T* x, long long ldx, bool vec,
+                        const float* factor, Mx4Out out, Mx4Out out_t) {
   launch_dependents();
   grid_dependency_wait();
   const Patch p = Patch::of<8>(cols);
@@ -499,7 +542,11 @@ __global__ void __launch_bounds__(kTileThreads)
 // a = act(gate) * up again. dg and dup leave quantised along the rows (for dX) and along the
 // columns (for dW1), a along the columns (for dW2); none of them is written in 16 bits. Patches of
 // 8 x 4: dg is quantised from registers while dup and a wait in shared memory, 16 bytes a lane,
-// each lane its own.
+// each lane its own. With all three in registers the same took 89 us instead of 81 (gelu 224
+// instead of 124), and patches of 8 x 8 that read the inputs once per result 140.
+//
+// Bound by instructions (five quantisations an element: 55 % of the ALU's peak): 2048 x 11008 silu
+// 75 / 91 us (mxfp4 / nvfp4; 195 MB, 2.6 TB/s), gelu 119 / 142 us.
 struct Quad {  // four consecutive bf16
   uint2 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int cols, bool row_ok,
@@ -507,14 +554,14 @@ struct Quad {  // four consecutive bf16
     a = make_uint2(0, 0);
     if (!row_ok || c >= cols) return;
     if (vec && c + 4 <= cols) {
-      a = __ldg(reinterpret_cast<const uint2*>(row + c));
+      a = ld8(row + c);
     } else if (c + 4 < cols) {  // the aligned words that hold them (see Vec8)
       const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
       const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
-      a = make_uint2(__ldg(w), __ldg(w + 1));
+      a = make_uint2(ld4(w), ld4(w + 1));
       if (at & 2) {
         a.x = prmt(a.x, a.y, 0x5432);
-        a.y = prmt(a.y, __ldg(w + 2), 0x5432);
+        a.y = prmt(a.y, ld4(w + 2), 0x5432);
       }
     } else {
       uint32_t h[4];
@@ -531,10 +578,10 @@ struct Quad {  // four consecutive bf16
 
 template <int FMT, int ACT>
 __global__ void __launch_bounds__(kTileThreads, 4)
-    mx4_gated_bwd_kernel(int rows, int F, const __nv_bfloat16* __restrict__ da,
-                         long long ldda, bool vec_da, const __nv_bfloat16* __restrict__ u,
-                         long long ldu, bool vec_g, bool vec_u, const float* __restrict__ f_du,
-                         const float* __restrict__ f_dut, const float* __restrict__ f_at,
+    mx4_gated_bwd_kernel(int rows, int F, const __nv_bfloat16* da,
+                         long long ldda, bool vec_da, const __nv_bfloat16* u,
+                         long long ldu, bool vec_g, bool vec_u, const float* f_du,
+                         const float* f_dut, const float* f_at,
                          Mx4Out dg, Mx4Out dup, Mx4Out dgt, Mx4Out dupt, Mx4Out at) {
   __shared__ float4 kept[2][8][kTileThreads];
   grid_dependency_wait();
@@ -592,12 +639,13 @@ __global__ void __launch_bounds__(kTileThreads, 4)
 
 // ---------------------------------------------------------------------------- and back
 // A lane decodes eight columns of eight rows, four rows apart, so that a warp's stores cover 128
-// consecutive bytes (bf16) of four rows.
+// consecutive bytes (bf16) of four rows. Bound by HBM, mostly by its own stores: 4096 x 11008 to
+// bf16 21 us (5.3 TB/s).
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kTileThreads)
-    mx4_dequantize_kernel(int rows, int cols, const uint8_t* __restrict__ codes,
-                          const uint8_t* __restrict__ scales, long long ld,
-                          const float* __restrict__ factor, T* __restrict__ y, long long ldy,
+    mx4_dequantize_kernel(int rows, int cols, const uint8_t* codes,
+                          const uint8_t* scales, long long ld,
+                          const float* factor, T* y, long long ldy,
                           bool vec) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -614,8 +662,8 @@ __global__ void __launch_bounds__(kTileThreads)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const bool ok = r0 + lr + 4 * i < rows;
-    w[i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(cp + i * 2 * ld)) : 0;
-    sb[i] = ok ? __ldg(sp + 64 * i) : 0;
+    w[i] = ok ? ld4(cp + i * 2 * ld) : 0;
+    sb[i] = ok ? sp[64 * i] : 0;
   }
   T* o = y + (r0 + lr) * ldy + c;
 #pragma unroll
@@ -696,17 +744,15 @@ cudaError_t dequantize_t(int rows, int cols, const Mx4Out& q, const float* facto
 
 cudaError_t launch_mx4_factor(int dtype, int rows, int cols, const void* x, long long ldx,
                               float* out, int num_sms, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(out, 0, 2 * sizeof(float), s);
+  cudaError_t e = launch_kernel(true, mx4_zero2_kernel, dim3(1), dim3(1), 0, s, out);
   if (e != cudaSuccess) return e;
   const unsigned long long n = (unsigned long long)rows * ((cols + 7) / 8);
   const dim3 grid(grid_for(n, 256 * 4, num_sms, 8));
   if (dtype)
-    mx4_factor_kernel<<<grid, 256, 0, s>>>(rows, cols, (const __nv_bfloat16*)x, ldx,
-                                           row_vec(x, ldx, 2), out);
-  else
-    mx4_factor_kernel<<<grid, 256, 0, s>>>(rows, cols, (const float*)x, ldx, row_vec(x, ldx, 4),
-                                           out);
-  return cudaGetLastError();
+    return launch_kernel(true, mx4_factor_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, rows, cols,
+                         (const __nv_bfloat16*)x, ldx, row_vec(x, ldx, 2), out);
+  return launch_kernel(true, mx4_factor_kernel<float>, grid, dim3(256), 0, s, rows, cols,
+                       (const float*)x, ldx, row_vec(x, ldx, 4), out);
 }
 
 cudaError_t launch_mx4_quantize(int fmt, int dtype, int rows, int cols, const void* x,
