@@ -259,9 +259,10 @@ mgt_status mgt_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* A, int64
  *              scale) may be any positive number, and a power of two keeps every rounding
  *              decision exact.
  *
- * mgt_mx4: one operand of `rows` by `cols`.
+ * mgt_mx4: one operand of `rows` by `cols`, each at least one.
  *   codes    rows of ld / 2 bytes, two elements to a byte, the even column in the low half.
- *            Columns from cols up to the next multiple of 128 hold zeros.
+ *            Columns from cols up to the next multiple of 128 are read by the products and hold
+ *            zeros, with any scale but NaN (every call that writes an operand writes them).
  *   scales   tiles of 128 rows by 4 blocks, 512 bytes each, row r and block b at byte
  *            16 (r % 32) + 4 (r % 128 / 32) + b % 4 of tile (r / 128) * (ld / (4 * block)) + b / 4:
  *            the order in which the tensor core takes them. Whole tiles of rows; those behind
@@ -332,8 +333,8 @@ mgt_status mgt_gemm_mx4_gated(const mgt_mx4* X, const mgt_mx4* W, int32_t act, c
 /* Backward of the gated product, quantised for the products that follow: from da = dL/da (bf16,
  * [rows][ffn]) and u = [gate | up] (bf16, as above), in fp32
  *   dgate = da * up * act'(gate),   dup = da * act(gate),   a = act(gate) * up
- * du  [rows][2 P]: dgate from column 0, dup from column P (zeros behind each): dX = du W1^T^T with
- *     W1^T laid out alike;
+ * du  [rows][2 P]: dgate from column 0, dup from column P (zeros behind each): with W1^T ([hidden][2 P],
+ *     quantised along its rows) laid out alike, dX = du (W1^T)^T is one mgt_gemm_mx4;
  * dut [2 P][rows]: dgate^T from row 0, dup^T from row P: the weight gradients of gate and up;
  * at  [ffn][rows]: a^T, for dW2. Any of them may be NULL, not all. MGT_NVFP4: factors are inputs. */
 mgt_status mgt_mx4_gated_bwd(int32_t act, int32_t rows, int32_t ffn, const void* da, int64_t ldda,

@@ -90,6 +90,27 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The operands' tensor factors on a sum: their product x, and y = 1. A product outside fp32's normal
+// numbers would make zero or infinity of sums that are neither (and NaN of zeros): there x and y
+// are the two factors, whose smaller one then is above one or whose larger one is below 2^23.
+template <int FMT>
+__device__ __forceinline__ float2 sum_factors(const float* a, const float* b) {
+  if constexpr (FMT == kMxfp4) return make_float2(1.f, 1.f);  // has none
+  const float fa = a[1], fb = b[1], f = fa * fb;
+  return f >= 1.17549435e-38f && f <= 3.40282347e38f ? make_float2(f, 1.f) : make_float2(fa, fb);
+}
+template <int FMT, int N>
+__device__ __forceinline__ void scale_sums(float (&v)[N], float2 f) {
+  if constexpr (FMT == kNvfp4) {
+    if (f.y != 1.f) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] *= f.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= f.x;
+  }
+}
+
 // v = act(v)
 template <int N>
 __device__ __forceinline__ void gate_all(float (&v)[N], int act) {
@@ -367,7 +388,7 @@ __global__ void __launch_bounds__(192)
   }
   if (epi && ok) {
     // A warp takes a token of its CTA's share at a time, a lane four neighbouring weight rows.
-    const float f = (g.p_factor ? g.p_factor[1] : 1.f) * (g.q_factor ? g.q_factor[1] : 1.f);
+    const float2 f = sum_factors<FMT>(g.p_factor, g.q_factor);
     const int tokens = min(g.bnq, g.M - q0);
     const uint32_t mine = smem_u32(part + lane * 4);
     const int col = p0 + lane * 4;
@@ -389,8 +410,7 @@ __global__ void __launch_bounds__(192)
             v[m][3] += w.w;
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[m][i] *= f;
+        scale_sums<FMT>(v[m], f);
       }
       const long long row = q0 + t;
       if constexpr (!GATED) {
@@ -800,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int ew = warp & 3, set = (warp - 2) >> 2;
     uint8_t* my = stg + (warp - 2) * kStoreBytes;
-    const float f = (g.a_factor ? g.a_factor[1] : 1.f) * (g.b_factor ? g.b_factor[1] : 1.f);
+    const float2 f = sum_factors<FMT>(g.a_factor, g.b_factor);
     const Mx4Factor of = mx4_factor<FMT>(GATED ? g.out_factor : nullptr);
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t overlap0 = mapa_shared(smem_u32(overlap), 0);
@@ -834,13 +854,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) reg_fence(r[i]);
+        if (FMT == kNvfp4 && f.y != 1.f) {  // (in place: further down it took registers)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) * f.y);
+        }
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          reg_fence(r[i]);
           const int col0 = nt * bn + chunk(i) * 32;
           if (i < count && col0 < g.N && row0 < g.M) {
             float v[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[i][k]) * f;
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[i][k]) * f.x;
             if (g.c_f32)
               store_block(my, turn, v, &tmO, static_cast<float*>(g.C), g.ldc, row0, g.M, col0, g.N,
                           g.tma);
@@ -862,11 +890,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_relaxed(i == 0 ? overlap0 : tempty0 + acc * 8);
           const int col0 = nt * 128 + c * 32;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            v[k] *= f;
-            w[k] *= f;
-          }
+          scale_sums<FMT>(v, f);
+          scale_sums<FMT>(w, f);
           if (g.u && row0 < g.M) {
             if (col0 < g.N) {
               store_block(my, turn, v, &tmO, g.u, g.ldu, row0, g.M, col0, g.N, g.tma);

@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(kTileThreads)
   const long long r0 = (long long)tr * kTileRows + warp * 32;
   const int c = (int)tc * 64 + (lane & 7) * 8;
   if (r0 >= rows || c >= cols) return;
-  const float f = FMT == kNvfp4 ? factor[1] : 1.f;
+  float f = 1.f;
+  if constexpr (FMT == kNvfp4) f = factor[1];
   const int lr = lane >> 3;
   const uint8_t* cp = codes + ((r0 + lr) * ld + c) / 2;
   const uint8_t* sp = scales + mx4_scale_off<FMT>(r0 + lr, c / Mx4Fmt<FMT>::kBlock, ld);
@@ -669,11 +670,11 @@ __global__ void __launch_bounds__(kTileThreads)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (r0 + lr + 4 * i >= rows) break;
-    const float s = mx4_scale_value<FMT>(sb[i]) * f;
+    const float s = mx4_scale_value<FMT>(sb[i]);
     float v[8];
     e2m1x8_values(w[i], v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= s;
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * s * f;  // (e2m1 times s is exact)
     T* e = o + (long long)(4 * i) * ldy;
     if (vec && c + 8 <= cols) {
       if constexpr (sizeof(T) == 2) {

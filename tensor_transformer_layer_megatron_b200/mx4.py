@@ -55,11 +55,11 @@ class Mx4:
         if fmt == "nvfp4" and factor is None:
             factor = torch.ones(2, dtype=torch.float32, device=codes.device)
         if factor is not None and (factor.dtype != torch.float32 or factor.numel() < 2 or
-                               not factor.is_contiguous()):
+                                   not factor.is_contiguous()):
             raise TypeError("factor must be two contiguous float32")
         for t in (scales, factor):
             if t is not None and t.device != codes.device:
-                  raise ValueError("codes, scales and factor must be on one device")
+                raise ValueError("codes, scales and factor must be on one device")
         self.fmt, self.rows, self.cols = fmt, rows, cols
         self.codes, self.scales, self.factor, self.device = codes, scales, factor, codes.device
         self.index = codes.get_device()
@@ -78,7 +78,9 @@ class Mx4:
 
     def part(self, row, rows, col, cols):
         """The operand of rows row .. row + rows - 1 and columns col .. col + cols - 1 of this
-        one, in the same buffers; row and col are multiples of 128."""
+        one, in the same buffers; row and col are multiples of 128. Where its columns end inside a
+        group of 128, a product reads the whole group, whose rest has to hold zeros, as it does
+        at the operand's end and in a part that was quantised into."""
         if row % 128 or col % 128 or row < 0 or col < 0 or rows < 1 or cols < 1 or \
             row + rows > self.rows or _up128(col + cols) > _up128(self.cols):
             raise ValueError("a part starts at multiples of 128 and lies inside the operand")

@@ -250,6 +250,49 @@ def test_quantize_with_a_factor_that_is_no_power_of_two():
     assert (np.abs(y - ref)[sure] <= 2.0 ** -22 * np.abs(ref)[sure]).all()
 
 
+@pytest.mark.parametrize("M", [5, 300])
+def test_factors_whose_product_leaves_fp32(M):
+    """f_a f_b = 2^-150 is no fp32 number, the results (about 2^-121) are; with f_a f_b = 2^140 a
+    sum of zeros stays zero. Of positive sums every partial one is below the result: 32 steps, at
+    most 4 units of 2^-23 each; u rounds to bf16."""
+    N, K, st = 130, 2048, torch.zeros(1, dtype=torch.int32, device="cuda")
+    bar = 32 * 4 * 2.0 ** -23
+    for fa, fb in ((2.0 ** -100, 2.0 ** -50), (2.0 ** 70, 2.0 ** 70)):
+        x, w = randn(M, K, seed=1).abs() * 512, randn(512, K, seed=2).abs() * 512
+        x[M // 2] = 0
+        A, W = (operand("nvfp4", t.shape[0], K, (t * f).cuda(), f) for t, f in ((x, fa), (w, fb)))
+        C, u = torch.empty(M, N, device="cuda"), torch.empty(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+        mgt.gemm_mx4(A, W.rows_view(0, N), C, st)
+        a = operand("nvfp4", M, N)
+        mgt.gemm_mx4_gated(A, W, a, st, u=u)
+        gate, up = (values_of(A).double() @ values_of(W.rows_view(r, N)).double().T for r in (0, 256))
+        assert (C[M // 2] == 0).all() and (u[M // 2] == 0).all()
+        assert (values_of(a)[M // 2] == 0).all()
+        if fa > 1:
+            rest = torch.arange(M, device="cuda") != M // 2
+            assert torch.isinf(C[rest]).all() and torch.isinf(u[rest]).all()
+        else:
+            assert ((C.double() - gate).abs() <= bar * gate).all()
+            both = torch.cat([gate, up], 1)
+            assert ((u.double() - both).abs() <= (2.0 ** -8 + 2 * bar) * both).all()
+    assert int(st) == 0
+
+
+def test_dequantised_zeros_of_a_block_beyond_fp32():
+    """448 f = 2^133.8 is no fp32 number; 0 * 448 f and 0.5 * 2^-9 f are."""
+    q = operand("nvfp4", 3, 64, f=2.0 ** 125, fill=0)
+    q.scales.fill_(0x7E)
+    for t in TYPES.values():
+        y = torch.empty(3, 64, dtype=t, device="cuda")
+        mgt.mx4_dequantize(q, y)
+        assert (y == 0).all()
+    q.codes.fill_(0x11)
+    q.scales.fill_(1)
+    y = torch.empty(3, 64, device="cuda")
+    mgt.mx4_dequantize(q, y)
+    assert (y == 2.0 ** 115).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_product_carries_infinities_and_nans(fmt):
     """A block that cannot be scaled makes the sums that it enters NaN, and no others."""
