@@ -1162,15 +1162,20 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
 // tiles hold 256 rows. N x K = 12288 x 4096: 96 rows 15.0 us against 15.3, 128 rows 16.4 against
 // 15.4; gated 11008 x 4096: 64 rows 18.9 against 22.3, 96 rows 25.8 against 22.5. Where the sum is
 // long and the pairs' tiles leave most SMs idle the split wins further up: 4096 x 11008, 128 rows
-// 16.9 against 22.2, 256 rows 21.2 against 22.7; and with six CTAs or more to a tile at any number
-// of rows: 512 x 512 x 8192 10.3 against 15.2, 1000 x 128 x 16384 11.6 against 25.6 (products alone).
+// 16.9 against 22.2, 256 rows 21.2 against 22.7; and at any number of rows, by the CTAs that a tile
+// of 256 x 128 can have and the 256-element stages of the sum (products alone; split against pairs):
+// with six or more from 20 stages up (512 x 512 x 8192 10.3 against 15.2, 1000 x 128 x 16384 11.6
+// against 25.6); with four 14.6 against 18.9 at 768 x 1024 x 11008 and 13.4 against 12.8 at 512 x 2048 x
+// 6144; with three 18.0 against 19.1 at 512 x 2560 x 11008 and 16.4 against 15.6 at K = 8192; with two
+// 32.8 against 36.1 at 1024 x 2048 x 24576 and 22.7 against 20.7 at K = 12288.
 bool few_rows(const Mx4Gemm& g, int num_sms) {
   if (g.gated) return g.M <= 64;
   if (g.M <= 96) return true;
   const long long tiles = (long long)((g.M + 255) / 256) * ((g.N + 127) / 128);
   const int ki = (g.K + kStageK - 1) / kStageK;
-  return (tiles * 6 * 10 <= 9 * num_sms && ki >= 20) ||
-         (g.M <= 256 && tiles <= num_sms / 4 && ki > 32);
+  if (g.M <= 256 && tiles <= num_sms / 4 && ki > 32) return true;
+  const long long ctas = 9 * num_sms / (10 * tiles);
+  return ctas >= 6 ? ki >= 20 : ki >= 24 && ki * (ctas - 1) > 80;
 }
 
 template <int FMT, bool GATED>

@@ -178,6 +178,25 @@ def values_of(q):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(300, 2000, 8100), (700, 1000, 6500), (300, 2700, 11000), (260, 4000, 21000),
+                                   (1000, 1999, 24500)])
+def test_product_of_long_sums(M, N, K, fmt):
+    """Sums split over two to five CTAs, and the same bytes from a second call."""
+    x, w = randn(M, K, seed=M).cuda(), randn(N, K, seed=N).cuda()
+    fx = 1.0 if fmt == "mxfp4" else 2.0 ** -8
+    A, B = operand(fmt, M, K, x, fx), operand(fmt, N, K, w, fx)
+    a, b, st = values_of(A), values_of(B), torch.zeros(1, dtype=torch.int32, device="cuda")
+    C = torch.full((M + 1, N + 3), 77.0, device="cuda")
+    mgt.gemm_mx4(A, B, C[:M, :N], st)
+    ref, most = a @ b.T, a.abs() @ b.abs().T  # bound: product_bound's, in fp32
+    assert ((C[:M, :N].double() - ref).abs() <= most * (4 * -(-K // 64) * 2.0 ** -23) + ref.abs() * 2.0 ** -23).all()
+    assert (C[M] == 77).all() and (C[:, N:] == 77).all() and int(st) == 0
+    D = torch.empty(M, N, device="cuda")
+    mgt.gemm_mx4(A, B, D, st)
+    assert torch.equal(C[:M, :N], D)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_product_of_every_row_count(fmt):
     """Row counts around every step of the few-row kernel's shapes, with a sum long enough that it
     keeps up to 256 rows, and around its end; against the dequantised operands in float64."""
