@@ -567,3 +567,39 @@ def test_streams_and_graphs_give_the_same_bytes(fmt):
         torch.cuda.synchronize()
         assert all(torch.equal(r.y, want[(k + turn) % 2]) for k, r in enumerate(runs))
     assert all(int(r.st) == 0 for r in runs)
+
+
+@pytest.mark.parametrize("M", [1, 40, 600])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_chains_over_the_same_buffers(fmt, M):
+    """Each call rewrites what the one before has read, or reads what it wrote, with nothing between
+    them on the stream: the same bytes as with a synchronisation after every call."""
+    F, K, st = 700, 1024, torch.zeros(1, dtype=torch.int32, device="cuda")
+    W, _, _ = gated_weights(fmt, F, K, 2.0 ** -10 if fmt == "nvfp4" else 1.0, seed=1)
+    w2 = operand(fmt, K, F, randn(K, F, seed=2, scale=0.1).cuda(), 2.0 ** -10)
+    du_w = operand(fmt, K, 2 * 768, randn(K, 2 * 768, seed=3, scale=0.05).cuda(), 2.0 ** -10)
+
+    def chain(wait):
+        x = randn(M, K, seed=4).bfloat16().cuda()
+        q, a, u = operand(fmt, M, K), operand(fmt, M, F, f=2.0 ** -8), torch.empty(M, 2 * F, dtype=torch.bfloat16, device="cuda")
+        da, du, at = torch.empty(M, F, dtype=torch.bfloat16, device="cuda"), operand(fmt, M, 2 * 768), operand(fmt, F, M)
+        qt = mgt.Mx4(fmt, K, M, factor=q.factor)
+        for _ in range(6):
+            for call in ([lambda: mgt.mx4_tensor_factor(x, q.factor)] if fmt == "nvfp4" else []) + [
+                    lambda: mgt.mx4_quantize(x, q, qt),
+                    lambda: mgt.gemm_mx4_gated(q, W, a, st, u=u),
+                    lambda: mgt.mx4_dequantize(a, da),
+                    lambda: mgt.gemm_mx4(a, w2, x, st),
+                    lambda: mgt.mx4_gated_bwd(da, u, du, None, at),
+                    lambda: mgt.gemm_mx4(du, du_w, x, st),
+                    lambda: mgt.mx4_dequantize(q, x)]:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [t.clone() for t in (x, u, da, q.codes, a.codes, du.codes, at.codes)]
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(g, w) for g, w in zip(chain(False), want))
+    assert int(st) == 0
