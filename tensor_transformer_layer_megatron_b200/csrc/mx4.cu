@@ -639,8 +639,9 @@ __global__ void __launch_bounds__(kTileThreads, 4)
 
 // ---------------------------------------------------------------------------- and back
 // A lane decodes eight columns of eight rows, four rows apart, so that a warp's stores cover 128
-// consecutive bytes (bf16) of four rows. Bound by HBM, mostly by its own stores: 4096 x 11008 to
-// bf16 21 us (5.3 TB/s).
+// consecutive bytes (bf16) of four rows. Rows of other alignment pass through shared memory, so that
+// a warp's lanes write consecutive elements. Bound by HBM, mostly by its own stores: 4096 x 11008 to
+// bf16 20 us (5.5 TB/s), 4096 x 11007 27 us (150 with the lanes' own eight elements one by one).
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kTileThreads)
     mx4_dequantize_kernel(int rows, int cols, const uint8_t* codes,
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kTileThreads)
   const unsigned tr = blockIdx.x / (unsigned)tiles_c, tc = blockIdx.x - tr * (unsigned)tiles_c;
   const long long r0 = (long long)tr * kTileRows + warp * 32;
   const int c = (int)tc * 64 + (lane & 7) * 8;
-  if (r0 >= rows || c >= cols) return;
+  if (r0 >= rows || (vec && c >= cols)) return;
   float f = 1.f;
   if constexpr (FMT == kNvfp4) f = factor[1];
   const int lr = lane >> 3;
@@ -662,21 +663,55 @@ __global__ void __launch_bounds__(kTileThreads)
   uint32_t w[8], sb[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const bool ok = r0 + lr + 4 * i < rows;
+    const bool ok = r0 + lr + 4 * i < rows && c < cols;
     w[i] = ok ? ld4(cp + i * 2 * ld) : 0;
     sb[i] = ok ? sp[64 * i] : 0;
+  }
+  auto values = [&](int i, float (&v)[8]) {
+    const float s = mx4_scale_value<FMT>(sb[i]);
+    e2m1x8_values(w[i], v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * s * f;  // (e2m1 times s is exact)
+  };
+  if (!vec) {
+    __shared__ __align__(16) T stage[kTileThreads / 32][4][64];
+    T(*st)[64] = stage[warp];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + 4 * i >= rows) break;
+      float v[8];
+      values(i, v);
+      T* d = &st[lr][(lane & 7) * 8];
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(d) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+      } else {
+        reinterpret_cast<float4*>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+      __syncwarp();
+      T e[8];  // all read before the first is written: shared loads stay behind global stores
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = st[j >> 1][(j & 1) * 32 + lane];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const long long row = r0 + 4 * i + (j >> 1);
+        const int col = (int)tc * 64 + (j & 1) * 32 + lane;
+        if (row < rows && col < cols) y[row * ldy + col] = e[j];
+      }
+    }
+    return;
   }
   T* o = y + (r0 + lr) * ldy + c;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (r0 + lr + 4 * i >= rows) break;
-    const float s = mx4_scale_value<FMT>(sb[i]);
     float v[8];
-    e2m1x8_values(w[i], v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * s * f;  // (e2m1 times s is exact)
+    values(i, v);
     T* e = o + (long long)(4 * i) * ldy;
-    if (vec && c + 8 <= cols) {
+    if (c + 8 <= cols) {
       if constexpr (sizeof(T) == 2) {
         uint4 b;
         b.x = pack_bf16x2(v[0], v[1]);
