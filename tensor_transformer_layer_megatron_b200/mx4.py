@@ -19,6 +19,11 @@ MX4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
+# Rows and columns of an operand, as the library has it. Sizes travel as int32, and ctypes cuts what
+# does not fit without a word, so larger ones are refused here.
+_MOST = 1 << 30
+
+
 def _up128(n):
     return (n + 127) // 128 * 128
 
@@ -35,6 +40,8 @@ class Mx4:
         rows, cols = int(rows), int(cols)
         if rows < 1 or cols < 1:
             raise ValueError("an operand has at least one row and one column")
+        if rows > _MOST or cols > _MOST:
+            raise ValueError("an operand has at most 2**30 rows and columns")
         block = 32 if fmt == "mxfp4" else 16
         if codes is None:
             codes = torch.empty(rows, _up128(cols) // 2, dtype=torch.uint8, device=device)
@@ -115,6 +122,8 @@ def _matrix(t, name):
     if len(shape) != 2:
         raise TypeError("%s must be 2-D with contiguous rows" % name)
     rows, cols = shape
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        raise ValueError("%s must have fewer than 2**31 rows and columns" % name)
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise TypeError("%s must be 2-D with contiguous rows" % name)

@@ -180,3 +180,20 @@ def test_python_checks_types_shapes_and_devices():
         mgt.mx4_gated_bwd(u[:, :50], u, a)
     with pytest.raises(TypeError):
         mgt.mx4_gated_bwd(u[:, :60].float(), u, a)
+
+
+def test_sizes_beyond_int32_are_refused():
+    """2^32 + 128 cut to 32 bits is 128: it must not arrive as that. ("meta" tensors have a shape only.)"""
+    many, empty = 2 ** 32 + 128, lambda *n, t=torch.uint8: torch.empty(*n, dtype=t, device="meta")  # noqa: E731
+    for rows, cols in ((many, 100), (100, many), (2 ** 30 + 1, 1), (1, 2 ** 30 + 1)):
+        with pytest.raises(ValueError, match="2\\*\\*30"):
+            mgt.Mx4("mxfp4", rows, cols, codes=empty(rows, (cols + 127) // 128 * 64))
+    assert mgt.Mx4("mxfp4", 1, 2 ** 30, codes=empty(1, 2 ** 29))._c.cols == 2 ** 30
+    f, small = empty(2, t=torch.float32), mgt.Mx4("mxfp4", 128, 128, device="cpu")
+    for shape in ((1, many), (many, 1), (2 ** 31, 1), (1, 2 ** 31)):
+        x = empty(*shape, t=torch.bfloat16)
+        for call in (lambda: mgt.mx4_tensor_factor(x, f), lambda: mgt.mx4_quantize(x, small),
+                     lambda: mgt.mx4_dequantize(small, x), lambda: mgt.gemm_mx4(small, small, x, None),
+                     lambda: mgt.mx4_gated_bwd(x, x, du=small)):
+            with pytest.raises(ValueError, match="2\\*\\*31"):
+                call()
