@@ -113,16 +113,19 @@ struct Vec8<float> {
   }
 };
 
+// Groups of eight columns; cols may be any positive int (cols + 7 may not be one).
+__host__ __device__ __forceinline__ int groups8(int cols) { return (cols - 1) / 8 + 1; }
+
 // Eight elements from column c of a row of `cols`; zeros behind the last column. vec: the row
-// base is 16-byte aligned (c is a multiple of 8).
+// base is 16-byte aligned (c is a multiple of 8). (c + 8 need not be an int.)
 template <typename T>
 __device__ __forceinline__ void load8(Vec8<T>& r, const T* row, int c, int cols, bool row_ok,
                                       bool vec) {
   if (!row_ok || c >= cols)
     r.zero();
-  else if (vec && c + 8 <= cols)
+  else if (vec && cols - c >= 8)
     r.load(row + c);
-  else if (c + 8 < cols)
+  else if (cols - c > 8)
     r.load_words(row + c);
   else
     r.load_n(row + c, cols - c);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, con
   grid_dependency_wait();
   uint32_t m = 0;
   constexpr int U = 4;
-  Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, (cols + 7) / 8);
+  Walk at(blockIdx.x * 256ull + threadIdx.x, gridDim.x * 256ull, groups8(cols));
   while (at.row < rows) {
     Vec8<T> w[U];
 #pragma unroll
@@ -782,7 +785,7 @@ cudaError_t launch_mx4_factor(int dtype, int rows, int cols, const void* x, long
                               float* out, int num_sms, cudaStream_t s) {
   cudaError_t e = launch_kernel(true, mx4_zero2_kernel, dim3(1), dim3(1), 0, s, out);
   if (e != cudaSuccess) return e;
-  const unsigned long long n = (unsigned long long)rows * ((cols + 7) / 8);
+  const unsigned long long n = (unsigned long long)rows * groups8(cols);
   const dim3 grid(grid_for(n, 256 * 4, num_sms, 8));
   if (dtype)
     return launch_kernel(true, mx4_factor_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, rows, cols,

@@ -603,3 +603,16 @@ def test_chains_over_the_same_buffers(fmt, M):
     for _ in range(5):
         assert all(torch.equal(g, w) for g, w in zip(chain(False), want))
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 2 ** 31 - 1), (1, 2 ** 31 - 8), (2, 2 ** 31 - 4), (2 ** 31 - 1, 1)])
+def test_factor_of_the_longest_rows_and_columns(rows, cols):
+    """Sizes at the end of int32, whose groups of eight columns end behind it; the largest element is
+    the last one, then the first."""
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    f = torch.empty(2, device="cuda")
+    for at, v in ((-1, 5000.0), (0, -9000.0)):
+        x.view(-1)[at] = v
+        mgt.mx4_tensor_factor(x, f)
+        amax, want = mx4.tensor_factor(np.array([[float(x.view(-1)[at])]]))
+        assert f.tolist() == [amax, want]
