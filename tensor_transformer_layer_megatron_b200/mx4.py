@@ -32,7 +32,13 @@ class Mx4:
     """A microscaled 4-bit operand of `rows` by `cols` (see mgt_mx4 in include/mgt_layer.h):
     device buffers for its codes [rows, ld / 2] and scale tiles, both uint8, and for "nvfp4" its
     factor {amax, f}, two fp32 on the device. Buffers are allocated (f = 1), or given: codes
-    with rows of ld / 2 contiguous bytes, `scales` with room for whole tiles of 128 rows."""
+    with rows of ld / 2 contiguous bytes, `scales` with room for whole tiles of 128 rows.
+
+    Calls go by the addresses taken here, so the attributes are read-only, but for `factor`: another
+    tensor assigned to it is the one that calls use from then on (graphs captured before, and parts
+    made before, keep the one they had)."""
+
+    _FIXED = ("fmt", "rows", "cols", "ld", "codes", "scales", "device", "index")
 
     def __init__(self, fmt, rows, cols, device="cuda", codes=None, scales=None, factor=None):
         if fmt not in MX4_FORMATS:
@@ -49,39 +55,54 @@ class Mx4:
             codes.stride(1) != 1 or (codes.shape[0] > 1 and
                                      codes.stride(0) != codes.shape[1]):
             raise TypeError("codes must be contiguous uint8 [rows, ld / 2]")
-        self.ld = 2 * codes.shape[1]
-        if self.ld % 128 or self.ld < _up128(cols):
+        ld = 2 * codes.shape[1]
+        if ld % 128 or ld < _up128(cols):
             raise ValueError("ld must be a multiple of 128 that holds all columns")
-        need = _up128(rows) * self.ld // block
+        need = _up128(rows) * ld // block
         if scales is None:
             scales = torch.empty(need, dtype=torch.uint8, device=codes.device)
         if scales.dtype != torch.uint8 or not scales.is_contiguous():
             raise TypeError("scales must be contiguous uint8")
         if scales.numel() < need:
             raise ValueError("scales need %d bytes" % need)
+        if scales.device != codes.device:
+            raise ValueError("codes, scales and factor must be on one device")
         if fmt == "nvfp4" and factor is None:
             factor = torch.ones(2, dtype=torch.float32, device=codes.device)
-        if factor is not None and (factor.dtype != torch.float32 or factor.numel() < 2 or
-                                   not factor.is_contiguous()):
-            raise TypeError("factor must be two contiguous float32")
-        for t in (scales, factor):
-            if t is not None and t.device != codes.device:
-                raise ValueError("codes, scales and factor must be on one device")
-        self.fmt, self.rows, self.cols = fmt, rows, cols
-        self.codes, self.scales, self.factor, self.device = codes, scales, factor, codes.device
-        self.index = codes.get_device()
+        self.__dict__.update(fmt=fmt, rows=rows, cols=cols, ld=ld, codes=codes,
+                             scales=scales, device=codes.device, index=codes.get_device())
+        self.__dict__["factor"] = self._factor(factor)
         self._bind(0, 0)
+
+    def _factor(self, t):
+        """t, checked as this operand's factor (None: an operand without one)."""
+        if t is None and self.fmt != "nvfp4":
+            return t
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.numel() < 2 or \
+            not t.is_contiguous():
+            raise TypeError("factor must be two contiguous float32")
+        if t.device != self.device:
+            raise ValueError("codes, scales and factor must be on one device")
+        return t
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED:
+            raise AttributeError("%s of an operand is fixed: make another one" % name)
+        if name == "factor":
+            self.__dict__["factor"] = self._factor(value)
+            self._bind(self._row, self._col)
+        else:
+            object.__setattr__(self, name, value)
 
     def _bind(self, row, col):
         block = 32 if self.fmt == "mxfp4" else 16
-        self._row, self._col = row, col
-        self._c = _Mx4Operand(
+        c = _Mx4Operand(
             MX4_FORMATS[self.fmt], self.rows, self.cols, self.ld,
             self.codes.data_ptr() + (row * self.ld + col) // 2,
             self.scales.data_ptr() + 512 * (row // 128 * (self.ld // (4 * block)) +
                                         col // (4 * block)),
             None if self.factor is None else self.factor.data_ptr())
-        self._addr = ctypes.addressof(self._c)
+        self.__dict__.update(_row=row, _col=col, _c=c, _addr=ctypes.addressof(c))
 
     def part(self, row, rows, col, cols):
         """The operand of rows row .. row + rows - 1 and columns col .. col + cols - 1 of this
@@ -92,9 +113,7 @@ class Mx4:
             row + rows > self.rows or _up128(col + cols) > _up128(self.cols):
             raise ValueError("a part starts at multiples of 128 and lies inside the operand")
         p = object.__new__(Mx4)
-        p.fmt, p.rows, p.cols, p.ld = self.fmt, int(rows), int(cols), self.ld
-        p.codes, p.scales, p.factor = self.codes, self.scales, self.factor
-        p.device, p.index = self.device, self.index
+        p.__dict__.update(self.__dict__, rows=int(rows), cols=int(cols))
         p._bind(self._row + row, self._col + col)
         return p
 
@@ -122,7 +141,7 @@ def _matrix(t, name):
     if len(shape) != 2:
         raise TypeError("%s must be 2-D with contiguous rows" % name)
     rows, cols = shape
-    if rows > 0x7fffffff or cols > 0x7fffffff:
+    if (rows | cols) >> 31:
         raise ValueError("%s must have fewer than 2**31 rows and columns" % name)
     ld, step = t.stride()
     if step != 1 and cols > 1:

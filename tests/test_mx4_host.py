@@ -197,3 +197,33 @@ def test_sizes_beyond_int32_are_refused():
                      lambda: mgt.mx4_gated_bwd(x, x, du=small)):
             with pytest.raises(ValueError, match="2\\*\\*31"):
                 call()
+
+
+def test_an_operand_follows_its_factor_and_keeps_the_rest():
+    """The calls take addresses: an assigned factor has to reach them, and nothing else may be assigned."""
+    mk = lambda fmt="nvfp4", **k: mgt.Mx4(fmt, 300, 200, device="cpu", **k)  # noqa: E731
+    q, t = mk(), torch.ones(2)
+    part = q.part(128, 100, 128, 72)
+    before = q.factor
+    q.factor = t
+    assert q.factor is t and q._c.factor == t.data_ptr() and q._addr == ctypes.addressof(q._c)
+    assert (q._c.codes, q._c.scales) == (q.codes.data_ptr(), q.scales.data_ptr())
+    assert part.factor is before and part._c.factor == before.data_ptr()
+    codes, scales = part._c.codes, part._c.scales
+    part.factor = t
+    assert (part._c.codes, part._c.scales, part._c.factor) == (codes, scales, t.data_ptr())
+    assert (part.rows, part.cols, part._c.rows, part._c.cols) == (100, 72, 100, 72)
+    for bad, error in ((None, TypeError), (2.0, TypeError), (torch.ones(1), TypeError),
+                       (torch.ones(2).double(), TypeError), (torch.ones(4)[::2], TypeError),
+                       (torch.ones(2, device="meta"), ValueError)):
+        with pytest.raises(error):
+            q.factor = bad
+        assert q.factor is t and q._c.factor == t.data_ptr()
+    for name in ("codes", "scales", "rows", "cols", "ld", "fmt", "device", "index"):
+        for operand in (q, part):
+            with pytest.raises(AttributeError):
+                setattr(operand, name, getattr(operand, name))
+    m = mk("mxfp4")
+    m.factor = t
+    m.factor = None
+    assert m._c.factor is None
