@@ -206,8 +206,14 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 template <int ACT>
 __device__ __forceinline__ void gate_and_grad(float z, float& h, float& dh) {
   if constexpr (ACT == 0) {
-    // e^-z and the reciprocal from the special-function unit (relative error about 2^-21 + |z| 2^-24)
-    silu_and_grad_bf16out(z, h, dh);
+    // sigmoid(z) = 2^-12 / (2^-12 + 2^-12 e^-z): the special-function unit's reciprocal is zero where
+    // its argument passes 2^126, which 1 + e^-z does at z = -87.3, where z sigmoid(z) is a normal
+    // number yet (down to -91.8); the scaled sum does at -95.7. Relative error about 2^-21 + |z| 2^-24
+    // (the exponent's product, ex2.approx, rcp.approx), far below the 2^-3 of an element. With expf
+    // and an IEEE division, within 2^-22, the backward of 2048 x 11008 took 93 us instead of 76.
+    const float s = 0x1p-12f * rcp_approx(0x1p-12f + ex2_approx(fmaf(z, -1.4426950408889634f, -12.0f)));
+    h = z * s;
+    dh = s * fmaf(z, 1.0f - s, 1.0f);
   } else if constexpr (ACT == 1) {
     const float c = 0.5f * erfcf(z * -0.7071067811865476f);
     h = z * c;

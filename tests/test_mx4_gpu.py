@@ -616,3 +616,45 @@ def test_factor_of_the_longest_rows_and_columns(rows, cols):
         mgt.mx4_tensor_factor(x, f)
         amax, want = mx4.tensor_factor(np.array([[float(x.view(-1)[at])]]))
         assert f.tolist() == [amax, want]
+
+
+TAIL = (-84.0, -87.0, -88.0, -89.0, -90.0, -91.0, -91.5, -92.0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_silu_far_in_its_negative_tail(fmt):
+    """silu(-88) = -88 e^-88 is a normal fp32 number, e^-88 is not. Blocks of one gate each. At -92,
+    e^z = 2^-132.7 has 16 bits left: two units for the exponential, half a one for the product with the
+    reciprocal make 2.5 * 2^-16.3 of the value, below 2^-14."""
+    M, F, up, eps = 32 * len(TAIL), 160, 2.0 ** 100, 2.0 ** -14
+    g = torch.tensor(TAIL).repeat_interleave(32).view(-1, 1).expand(M, F)
+    uv, da = randn(M, F, seed=1, scale=up).bfloat16(), randn(M, F, seed=2, scale=2.0 ** 20).bfloat16()
+    u = torch.cat([g.bfloat16(), uv], 1).contiguous().cuda()
+    dg, dup, a = mx4.gated_bwd(np64(da), np64(g), np64(uv), "silu")
+    for name, row, want, f in (("at", 0, a.T, 2.0 ** -24), ("dut", 0, dg.T, 2.0 ** -2), ("dut", 256, dup.T, 2.0 ** -104)):
+        f = f if fmt == "nvfp4" else 1.0  # (of dgate and dup, 2^100 apart, the one that it is for counts)
+        q = operand(fmt, F if name == "at" else 512, M, f=f)
+        mgt.mx4_gated_bwd(da.cuda(), u, **{name: q}, act="silu")
+        check_near(q.rows_view(row, F), want, f, eps, most=0.01)
+
+
+@pytest.mark.parametrize("M", [8, 320])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gated_product_far_in_the_negative_tail(fmt, M):
+    """The same through the products' epilogues, on gates that are sums of a few exact products."""
+    F, K, up = 40, 256, 2.0 ** 100 if fmt == "mxfp4" else 2.0 ** 10
+    x, w = torch.zeros(M, K), torch.zeros(256, K)
+    for m in range(M):  # numbers 6 * 2^k alone in their blocks, which both formats hold
+        x[m, 0], x[m, 32], x[m, 64], x[m, 96] = -96, -12, -6, (0, -0.75, -1.5, -3, -6)[m % 5]
+        x[m, 128] = 0.75 * (1 + m % 2)
+    w[:F, :128] = 0.75
+    w[128:128 + F, 128] = up * 1.5 * 0.5 ** (torch.arange(F) % 6)
+    X, W = operand(fmt, M, K, x.cuda()), operand(fmt, 256, K, w.cuda())
+    gate, upv = (np64(values_of(X) @ values_of(W.rows_view(r, F)).T) for r in (0, 128))
+    assert (np.unique(gate) == [-90, -87.75, -86.625, -86.0625, -85.5]).all()
+    f = 1.0 if fmt == "mxfp4" else 2.0 ** -117
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = operand(fmt, M, F, f=f)
+    mgt.gemm_mx4_gated(X, W, a, st, act="silu")
+    check_near(a, mx4.act(gate, "silu")[0] * upv, f, 2.0 ** -14, most=0.01)
+    assert int(st) == 0
