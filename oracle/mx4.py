@@ -109,9 +109,11 @@ def act(z, name):
     if name == "gelu":
         c = 0.5 * erfc(-z / np.sqrt(2))
         return z * c, c + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
-    k = np.sqrt(2 / np.pi)
-    t = np.tanh(k * (z + 0.044715 * z ** 3))
-    return 0.5 * z * (1 + t), 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * k * (1 + 3 * 0.044715 * z * z)
+    # (1 + tanh y) / 2 = 1 / (1 + e^-2y): 1 + tanh y is zero in 64 bits from y = -19 on, the value is not
+    w = 2 * np.sqrt(2 / np.pi)
+    with np.errstate(over="ignore"):
+        s = 1 / (1 + np.exp(-w * (z + 0.044715 * z ** 3)))
+    return z * s, s * (1 + z * (1 - s) * w * (1 + 3 * 0.044715 * z * z))
 
 
 def gated_bwd(da, g, u, name):

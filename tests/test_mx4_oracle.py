@@ -75,3 +75,15 @@ def test_gated_gradients_match_differences(name):
             e[i, j] = h
             assert abs((loss(g + e, u) - loss(g - e, u)) / (2 * h) - dg[i, j]) < 1e-8
             assert abs((loss(g, u + e) - loss(g, u - e)) / (2 * h) - du[i, j]) < 1e-8
+
+
+def test_tanh_gelu_keeps_its_negative_tail():
+    """(1 + tanh y) / 2 from decimal arithmetic at 60 digits, where 1 + tanh y cancels in 64 bits."""
+    import decimal
+    with decimal.localcontext(decimal.Context(prec=60)):
+        for z in (-3.0, -6.0, -10.0):
+            d = decimal.Decimal(z)
+            pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+            y = (2 / pi).sqrt() * (d + decimal.Decimal("0.044715") * d ** 3)
+            want = d / (1 + (-2 * y).exp())
+            assert abs(decimal.Decimal(float(mx4.act(z, "gelu_tanh")[0])) / want - 1) < 1e-13
