@@ -199,6 +199,13 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// z cut off at +-most (a positive number); NaN stays NaN.
+__device__ __forceinline__ float cut_off(float z, float most) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(most));
+  return r;
+}
+
 // Activation of a gated block and its derivative. ACT: 0 silu, 1 gelu (erf), 2 gelu (tanh). A
 // block's scale follows its largest value, so a value counts by its relative error however small
 // it is: Phi(z) = erfc(-z / sqrt 2) / 2 and (1 + tanh y) / 2 = 1 / (1 + e^-2y) keep it in the
@@ -220,10 +227,14 @@ __device__ __forceinline__ void gate_and_grad(float z, float& h, float& dh) {
     dh = fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), c);
   } else {
     const float k = 0.7978845608028654f;  // sqrt(2 / pi)
-    const float z2 = z * z;
-    const float s = 1.0f / (1.0f + expf(-2.0f * k * z * fmaf(0.044715f, z2, 1.0f)));
+    // At |z| = 64, s is 0 or 1 to every bit and dh is s. What they are made of is taken there beyond,
+    // where z^2 and z^3 would overflow and make NaN of 0 * inf (a NaN stays one). The quarter: 1 + e^-2y
+    // overflows at -2y = 88.7, where z s is a normal number yet (up to 89.6).
+    const float b = cut_off(z, 64.0f), b2 = b * b;
+    const float s =
+        0.25f * (1.0f / (0.25f + expf(fmaf(-2.0f * k * b, fmaf(0.044715f, b2, 1.0f), -1.3862944f))));
     h = z * s;
-    dh = s * fmaf(z * (1.0f - s), 2.0f * k * fmaf(0.134145f, z2, 1.0f), 1.0f);
+    dh = s * fmaf(b * (1.0f - s), 2.0f * k * fmaf(0.134145f, b2, 1.0f), 1.0f);
   }
 }
 

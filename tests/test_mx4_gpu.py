@@ -658,3 +658,61 @@ def test_gated_product_far_in_the_negative_tail(fmt, M):
     mgt.gemm_mx4_gated(X, W, a, st, act="silu")
     check_near(a, mx4.act(gate, "silu")[0] * upv, f, 2.0 ** -14, most=0.01)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gated_backward_at_huge_gates(fmt, act):
+    """Where act' is 0 or 1 to every bit the gradients are 0 or da * up, however large the gate: blocks of
+    one gate each. Nearer, at +-10, three fp32 products and an activation: 2^-17, as above."""
+    gates = [s * g for g in (10.0, 1e4, 1e13, 1.5e14, 1e19, 1e30) for s in (1, -1)]
+    M, F = 32 * len(gates), 70
+    g = torch.tensor(gates).repeat_interleave(32).view(-1, 1).expand(M, F).bfloat16()
+    uv, da = randn(M, F, seed=1, scale=2.0 ** -40).bfloat16(), randn(M, F, seed=2).bfloat16()
+    u = torch.cat([g, uv], 1).contiguous().cuda()
+    with np.errstate(over="ignore"):
+        dg, dup, a = mx4.gated_bwd(np64(da), np64(g), np64(uv), act)
+    fd, fa = (1.0, 1.0) if fmt == "mxfp4" else (2.0 ** -50, 2.0 ** 30)
+    du, dut, at = operand(fmt, M, 256, f=fd), operand(fmt, 256, M, f=fd), operand(fmt, F, M, f=fa)
+    mgt.mx4_gated_bwd(da.cuda(), u, du, dut, at, act=act)
+    for q, want, f in ((du.part(0, M, 0, F), dg, fd), (du.part(0, M, 128, F), dup, fd), (dut.rows_view(0, F), dg.T, fd),
+                       (dut.rows_view(128, F), dup.T, fd), (at, a.T, fa)):
+        assert torch.isfinite(values_of(q)).all()
+        check_near(q, want, f, 2.0 ** -17)
+
+
+@pytest.mark.parametrize("act,tail", [("gelu", (-11.0, -12.5, -12.875)), ("gelu_tanh", (-9.5, -10.0, -10.0625))])
+def test_gelu_far_in_its_negative_tail(act, tail):
+    """Both forms as far as their values are normal fp32 numbers (2^-125 at the last gates). The exponent is 88
+    there, of three roundings, 2^-16 of the value in all, and what multiplies z has 19 bits left or more:
+    2^-14 covers both."""
+    M, F, up, eps = 32 * len(tail), 160, 2.0 ** 100, 2.0 ** -14
+    g = torch.tensor(tail).repeat_interleave(32).view(-1, 1).expand(M, F)
+    uv, da = randn(M, F, seed=1, scale=up).bfloat16(), randn(M, F, seed=2, scale=2.0 ** 20).bfloat16()
+    u = torch.cat([g.bfloat16(), uv], 1).contiguous().cuda()
+    dg, dup, a = mx4.gated_bwd(np64(da), np64(g), np64(uv), act)
+    for name, row, want in (("at", 0, a), ("dut", 0, dg), ("dut", 256, dup)):
+        q = operand("mxfp4", F if name == "at" else 512, M)
+        mgt.mx4_gated_bwd(da.cuda(), u, **{name: q}, act=act)
+        check_near(q.rows_view(row, F), want.T, 1.0, eps, most=0.01)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gated_backward_carries_nan_gates(fmt, act):
+    """A NaN gate makes its block of every result NaN, and no other."""
+    M, F = 128, 192
+    da, u = randn(M, F, seed=1).bfloat16(), randn(M, 2 * F, seed=2).bfloat16()
+    u[70, 100] = float("nan")
+    ops = operand(fmt, M, 512), operand(fmt, 512, M), operand(fmt, F, M)
+    mgt.mx4_gated_bwd(da.cuda(), u.cuda(), *ops, act=act)
+    n = mx4.BLOCK[fmt]
+    r, c = slice(70 // n * n, 70 // n * n + n), slice(100 // n * n, 100 // n * n + n)
+    for k, q in enumerate((ops[0].part(0, M, 0, F), ops[0].part(0, M, 256, F), ops[1].rows_view(0, F), ops[1].rows_view(256, F),
+                           ops[2])):
+        want = np.zeros((M, F), bool)
+        if k < 2:
+            want[70, c] = True
+        else:
+            want[r, 100] = True
+        assert np.array_equal(np.isnan(np64(values_of(q))), want if k < 2 else want.T), k
