@@ -410,11 +410,13 @@ __device__ __forceinline__ void put_col_scales(const uint32_t (&b)[PC], uint8_t*
 }
 
 // Quantise a patch along its rows (into `out`) and / or its columns (into `out_t`); an operand
-// without codes is left out.
+// without codes, or that is switched off, is left out. f and ft may differ, but not be apart (see
+// factors_apart).
 template <int FMT, bool PACKED, bool ROWS, bool COLS, typename P>
 __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, int cols, int kp,
                                                const Mx4Out& out, const Mx4Out& out_t, Mx4Factor f,
-                                               Mx4Factor ft) {
+                                               Mx4Factor ft, bool rows_on = true,
+                                               bool cols_on = true) {
   constexpr int B = Mx4Fmt<FMT>::kBlock, PC = P::kCols;
   uint32_t rm[8], cm[PC];
   x.max_bits(rm, cm);
@@ -449,7 +451,8 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
   // row scales: of the warp's first block; column scales: of this lane's
   const PatchOut o = PatchOut::of<FMT>(out, p.r, p.c, p.c - (threadIdx.x & 7) * PC);
   const PatchOut t = PatchOut::of<FMT>(out_t, p.c, p.r, p.r);
-  const bool put_rows = ROWS && out.codes && p.c < kp;
+  const bool put_rows = ROWS && rows_on && out.codes && p.c < kp;
+  const bool put_cols = COLS && cols_on && out_t.codes;
   uint64_t cinv[PC / 2], cfs[PC / 2];
   uint32_t cc[PC], cmask[PC];
   if constexpr (COLS) {
@@ -463,7 +466,7 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
       cm[2 * q] = a.byte;
       cm[2 * q + 1] = b.byte;
     }
-    put_col_scales<PC, B / 8>(cm, t.scale, out_t.codes ? cols - p.c : 0);
+    put_col_scales<PC, B / 8>(cm, t.scale, put_cols ? cols - p.c : 0);
   }
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
@@ -502,7 +505,7 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
     }
   }
   if constexpr (COLS) {
-    if (out_t.codes) {
+    if (put_cols) {
 #pragma unroll
       for (int j = 0; j < PC; ++j)
         if (p.c + j < cols)
@@ -550,6 +553,13 @@ __global__ void __launch_bounds__(kTileThreads)
 //
 // Bound by instructions (five quantisations an element: 55 % of the ALU's peak): 2048 x 11008 silu
 // 75 / 91 us (mxfp4 / nvfp4; 195 MB, 2.6 TB/s), gelu 119 / 142 us.
+//
+// du and dut have a factor each. Elements that saturate are cut off by the larger one (see
+// quantize_patch), which is enough for the other as long as their quotient stays an fp32 number.
+__device__ __forceinline__ bool factors_apart(const Mx4Factor& a, const Mx4Factor& b) {
+  return a.tiny != b.tiny || fmaxf(a.f, b.f) > 1.8446744e19f * fminf(a.f, b.f);
+}
+
 struct Quad {  // four consecutive bf16
   uint2 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int c, int cols, bool row_ok,
@@ -588,55 +598,68 @@ __global__ void __launch_bounds__(kTileThreads, 4)
                          Mx4Out dg, Mx4Out dup, Mx4Out dgt, Mx4Out dupt, Mx4Out at) {
   __shared__ float4 kept[2][8][kTileThreads];
   grid_dependency_wait();
-  const Patch p = Patch::of<4>(F);
-  Quad wd[8], wg[8], wu[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const long long row = p.r + i;
-    wd[i].load(da + row * ldda, p.c, F, row < rows, vec_da);
-    wg[i].load(u + row * ldu, p.c, F, row < rows, vec_g);
-    wu[i].load(u + row * ldu + F, p.c, F, row < rows, vec_u);
-  }
-  const Mx4Factor fr = mx4_factor<FMT>(dg.codes ? f_du : nullptr);
-  const Mx4Factor fc = mx4_factor<FMT>(dgt.codes ? f_dut : nullptr);
-  const Mx4Factor fa = mx4_factor<FMT>(at.codes ? f_at : nullptr);
   const int kp = (F + 127) & ~127;
-  PatchF32<4> v;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float b[4], a[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float h, dh;
-      gate_and_grad<ACT>(wg[i].at(j), h, dh);
-      const float d = wd[i].at(j), up = wu[i].at(j);
-      v.v[i][j] = d * up * dh;
-      b[j] = d * h;
-      a[j] = h * up;
-    }
-    kept[0][i][threadIdx.x] = make_float4(b[0], b[1], b[2], b[3]);
-    kept[1][i][threadIdx.x] = make_float4(a[0], a[1], a[2], a[3]);
-  }
-  asm volatile("" ::: "memory");  // (or the compiler keeps them in registers after all)
-  auto take = [&](int k) {
+  if (!dg.codes) f_du = f_dut;
+  if (!dgt.codes) f_dut = f_du;
+  // Once, or where the factors are apart once for the rows and once for the columns.
+#pragma unroll 1
+  for (bool again = false;; again = true) {
+    Patch p = Patch::of<4>(F);
+    if (FMT == kNvfp4)  // (or all addresses are kept for the second turn)
+      asm volatile("" : "+r"(p.c), "+l"(p.r));
+    Quad wd[8], wg[8], wu[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 w = kept[k][i][threadIdx.x];
-      v.v[i][0] = w.x;
-      v.v[i][1] = w.y;
-      v.v[i][2] = w.z;
-      v.v[i][3] = w.w;
+      const long long row = p.r + i;
+      wd[i].load(da + row * ldda, p.c, F, row < rows, vec_da);
+      wg[i].load(u + row * ldu, p.c, F, row < rows, vec_g);
+      wu[i].load(u + row * ldu + F, p.c, F, row < rows, vec_u);
     }
-  };
-  constexpr bool kPacked = FMT == kMxfp4;
-  if (dg.codes || dgt.codes) {
-    quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dg, dgt, fr, fc);
-    take(0);
-    quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dup, dupt, fr, fc);
-  }
-  if (at.codes) {
-    take(1);
-    quantize_patch<FMT, kPacked, false, true>(v, p, rows, F, kp, at, at, fa, fa);
+    Mx4Factor fr = mx4_factor<FMT>(f_du), fc = mx4_factor<FMT>(f_dut);
+    const bool apart = FMT == kNvfp4 && factors_apart(fr, fc);
+    const bool rows_on = !again, cols_on = again || !apart;
+    if (apart) (again ? fr : fc) = again ? fc : fr;
+    PatchF32<4> v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float b[4], a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float h, dh;
+        gate_and_grad<ACT>(wg[i].at(j), h, dh);
+        const float d = wd[i].at(j), up = wu[i].at(j);
+        v.v[i][j] = d * up * dh;
+        b[j] = d * h;
+        a[j] = h * up;
+      }
+      kept[0][i][threadIdx.x] = make_float4(b[0], b[1], b[2], b[3]);
+      kept[1][i][threadIdx.x] = make_float4(a[0], a[1], a[2], a[3]);
+    }
+    asm volatile("" ::: "memory");  // (or the compiler keeps them in registers after all)
+    auto take = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 w = kept[k][i][threadIdx.x];
+        v.v[i][0] = w.x;
+        v.v[i][1] = w.y;
+        v.v[i][2] = w.z;
+        v.v[i][3] = w.w;
+      }
+    };
+    constexpr bool kPacked = FMT == kMxfp4;
+    if (dg.codes || dgt.codes) {
+      quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dg, dgt, fr, fc, rows_on, cols_on);
+      take(0);
+      quantize_patch<FMT, kPacked, true, true>(v, p, rows, F, kp, dup, dupt, fr, fc, rows_on,
+                                               cols_on);
+    }
+    if (!cols_on) continue;
+    if (at.codes) {
+      take(1);
+      const Mx4Factor fa = mx4_factor<FMT>(f_at);
+      quantize_patch<FMT, kPacked, false, true>(v, p, rows, F, kp, at, at, fa, fa);
+    }
+    return;
   }
 }
 

@@ -716,3 +716,30 @@ def test_gated_backward_carries_nan_gates(fmt, act):
         else:
             want[r, 100] = True
         assert np.array_equal(np.isnan(np64(values_of(q))), want if k < 2 else want.T), k
+
+
+@pytest.mark.parametrize("fd,ft", [(2.0 ** 90, 2.0 ** -60), (2.0 ** -60, 2.0 ** 90), (2.0 ** 60, 2.0 ** -120),
+                                   (2.0 ** -120, 2.0 ** 60),
+                                   (2.0 ** -20, 2.0 ** -14)])
+def test_gated_backward_with_factors_far_apart(fd, ft):
+    """du and dut each have a factor of their own: each is what it is alone, and saturates or vanishes with
+    the right sign where its factor is far off."""
+    M, F, act, eps = 70, 150, "silu", 2.0 ** -17
+    size = 2.0 ** 8 * max(fd, ft) if max(fd, ft) < 2.0 ** 100 else 2.0 ** 112
+    da, u = randn(M, F, seed=1, scale=size).bfloat16(), randn(M, 2 * F, seed=2).bfloat16()
+    dad, ud = da.cuda(), u.cuda()
+    dg, dup, a = mx4.gated_bwd(np64(da), np64(u[:, :F]), np64(u[:, F:]), act)
+    ops = lambda: (operand("nvfp4", M, 512, f=fd), operand("nvfp4", 512, M, f=ft))  # noqa: E731
+    (du, dut), (d1, t1), (d2, t2) = ops(), ops(), ops()
+    at = operand("nvfp4", F, M, f=2.0 ** -8)
+    mgt.mx4_gated_bwd(dad, ud, du, dut, at, act=act)
+    mgt.mx4_gated_bwd(dad, ud, du=d1, act=act)
+    mgt.mx4_gated_bwd(dad, ud, dut=t1, act=act)
+    mgt.mx4_gated_bwd(dad, ud, d2, t2, act=act)
+    for q, others, f in ((du, (d1, d2), fd), (dut, (t1, t2), ft)):
+        for o in others:
+            assert torch.equal(q.codes, o.codes) and torch.equal(q.scales, o.scales)
+        for row, want in ((0, dg), (256, dup)):
+            part = q.part(0, M, row, F) if q is du else q.rows_view(row, F)
+            check_near(part, want if q is du else want.T, f, eps)
+    check_near(at, a.T, 2.0 ** -8, eps)
