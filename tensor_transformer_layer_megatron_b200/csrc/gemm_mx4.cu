@@ -427,10 +427,11 @@ __global__ void __launch_bounds__(192)
         uint32_t mx = 0;
         gate_all(v[0], g.act);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = col + i < g.N ? v[0][i] * v[NM - 1][i] : 0.f;  // columns behind the last are zeros
-          mx = max(mx, abs_bits(a[i]));
-        }
+        for (int i = 0; i < 4; ++i)  // columns behind the last are zeros
+          a[i] = col + i < g.N ? v[0][i] * v[NM - 1][i] : 0.f;
+        if (FMT == kNvfp4 && of.tiny) mx4_lift(a, of);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = max(mx, abs_bits(a[i]));
         constexpr int B = Mx4Fmt<FMT>::kBlock;
 #pragma unroll
         for (int o = B / 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -904,6 +905,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const int live = row < g.M ? g.N - col0 : 0;
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = k < live ? v[k] * w[k] : 0.f;
+          if (FMT == kNvfp4 && of.tiny) mx4_lift(v, of);
           constexpr int B = Mx4Fmt<FMT>::kBlock;
           uint32_t codes[4], bytes = 0;
 #pragma unroll

@@ -424,15 +424,14 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
   if constexpr (COLS) lanes_max<PACKED, PC, B / 8>(cm, 8);
   if constexpr (FMT == kNvfp4) {
     // Rare: a kept factor far too small (elements beyond 4096 f saturate wherever they lie, so
-    // they may be cut off there before a quotient overflows), or a factor so small that f s would
-    // be subnormal (everything times 2^64).
+    // they may be cut off there before a quotient overflows), or a tiny one (see mx4_factor).
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
     const float f0 = ROWS && COLS ? fmaxf(f.f, ft.f) : ROWS ? f.f : ft.f;
-    const bool tiny = (ROWS && f.tiny) || (COLS && ft.tiny);
+    const bool tiny = ROWS ? f.tiny : ft.tiny;  // (both or neither)
     if (tiny || m > __float_as_uint(4096.0f * f0)) {
-      const float lim = 4096.0f * f0, k = tiny ? 1.8446744e19f : 1.0f;
+      const float k = tiny ? kLift : 1.0f, lim = 4096.0f * (f0 * (1.0f / k));
       auto cut = [&](float v) { return fminf(fmaxf(v, -lim), lim) * k; };
       auto cut_bits = [&](uint32_t b) {
         return b >= 0x7f800000u ? b : __float_as_uint(fminf(__uint_as_float(b), lim) * k);
@@ -442,10 +441,6 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
       for (int i = 0; i < 8; ++i) rm[i] = cut_bits(rm[i]);
 #pragma unroll
       for (int j = 0; j < PC; ++j) cm[j] = cut_bits(cm[j]);
-      f.f *= k;
-      f.inv *= 1.0f / k;
-      ft.f *= k;
-      ft.inv *= 1.0f / k;
     }
   }
   // row scales: of the warp's first block; column scales: of this lane's
@@ -514,8 +509,9 @@ __device__ __forceinline__ void quantize_patch(P& x, const Patch& p, int rows, i
   }
 }
 
+// (nvfp4 from fp32 both ways asks for four CTAs an SM, 128 registers: left alone it took 134 to 166.)
 template <int FMT, typename T, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, FMT == kNvfp4 && ROWS && COLS && sizeof(T) == 4 ? 4 : 0)
     mx4_quantize_kernel(int rows, int cols, const T* x, long long ldx, bool vec,
                         const float* factor, Mx4Out out, Mx4Out out_t) {
   launch_dependents();
@@ -557,7 +553,7 @@ __global__ void __launch_bounds__(kTileThreads)
 // du and dut have a factor each. Elements that saturate are cut off by the larger one (see
 // quantize_patch), which is enough for the other as long as their quotient stays an fp32 number.
 __device__ __forceinline__ bool factors_apart(const Mx4Factor& a, const Mx4Factor& b) {
-  return a.tiny != b.tiny || fmaxf(a.f, b.f) > 1.8446744e19f * fminf(a.f, b.f);
+  return a.tiny != b.tiny || fmaxf(a.f, b.f) > kLift * fminf(a.f, b.f);
 }
 
 struct Quad {  // four consecutive bf16

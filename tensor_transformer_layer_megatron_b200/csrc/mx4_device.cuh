@@ -58,20 +58,34 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
   }
 }
 
-// Tensor factor as the quantisers use it.
+// Tensor factor as the quantisers use it. Below 2^-100 the factor times a scale could be subnormal,
+// and below 2^-128 its reciprocal is no fp32 number: such a factor is `tiny`, f and inv are those of
+// 2^64 times it, and what it divides has to be multiplied by 2^64 first (mx4_lift, or in a patch by
+// quantize_patch).
+constexpr float kLift = 1.8446744e19f;  // 2^64
 struct Mx4Factor {
   float f, inv;
-  bool tiny;  // f below 2^-100: f s could be subnormal
+  bool tiny;
 };
 template <int FMT>
 __device__ __forceinline__ Mx4Factor mx4_factor(const float* factor) {
   Mx4Factor t = {1.f, 1.f, false};
   if (FMT == kNvfp4 && factor) {
     t.f = factor[1];
-    t.inv = 1.0f / t.f;
     t.tiny = t.f < 7.8886091e-31f;
+    if (t.tiny) t.f *= kLift;
+    t.inv = 1.0f / t.f;
   }
   return t;
+}
+// Values for a tiny factor: times 2^64; those beyond 4096 f saturate wherever they lie and are cut off
+// there, infinities and NaN stay.
+template <int N>
+__device__ __forceinline__ void mx4_lift(float (&v)[N], const Mx4Factor& f) {
+  const float most = 4096.0f * f.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (fabsf(v[i]) <= 3.4028234e38f) v[i] = fminf(fmaxf(v[i] * kLift, -most), most);
 }
 
 // What a block's elements are multiplied by, and the byte that stands for its scale.
@@ -113,7 +127,7 @@ __device__ __forceinline__ Mx4Block mx4_block(uint32_t amax_bits, const Mx4Facto
     q.mask = (bad || s == 0.f) ? 0u : 0xffffffffu;
     q.fs = f.f * s;
     q.inv = q.mask ? f.inv * rcp_approx(s) : 0.f;
-    q.wide = f.tiny || t > 896.0f;
+    q.wide = t > 896.0f;
   }
   return q;
 }
@@ -128,8 +142,8 @@ __device__ __forceinline__ float mx4_scaled(float x, const Mx4Block& q) {
   if constexpr (FMT == kMxfp4) return y;
   return fmaf(fmaf(-y, q.fs, x), q.inv, y);
 }
-// The same for a block whose quotients may overflow (a kept factor far too small: they saturate)
-// or whose f s may be subnormal: first x / f, clamped to fp32's range, then by s.
+// The same for a block whose quotients may overflow (a kept factor far too small: they saturate):
+// first x / f, clamped to fp32's range, then by s.
 __device__ __forceinline__ float mx4_scaled_wide(float x, uint32_t byte, float inv_f) {
   return fmaxf(fminf(x * inv_f, 3.4028234e38f), -3.4028234e38f) /
          mx4_scale_value<kNvfp4>(byte);

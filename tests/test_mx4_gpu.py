@@ -719,7 +719,7 @@ def test_gated_backward_carries_nan_gates(fmt, act):
 
 
 @pytest.mark.parametrize("fd,ft", [(2.0 ** 90, 2.0 ** -60), (2.0 ** -60, 2.0 ** 90), (2.0 ** 60, 2.0 ** -120),
-                                   (2.0 ** -120, 2.0 ** 60),
+                                   (2.0 ** -120, 2.0 ** 60), (2.0 ** -10, 2.0 ** -130), (2.0 ** -149, 2.0 ** 120),
                                    (2.0 ** -20, 2.0 ** -14)])
 def test_gated_backward_with_factors_far_apart(fd, ft):
     """du and dut each have a factor of their own: each is what it is alone, and saturates or vanishes with
@@ -743,3 +743,49 @@ def test_gated_backward_with_factors_far_apart(fd, ft):
             part = q.part(0, M, row, F) if q is du else q.rows_view(row, F)
             check_near(part, want if q is du else want.T, f, eps)
     check_near(at, a.T, 2.0 ** -8, eps)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("f", [2.0 ** -149, 2.0 ** -140, 2.0 ** -128, 2.0 ** -127, 2.0 ** -110])
+def test_factors_below_the_normal_numbers(f, dtype):
+    """A kept factor whose reciprocal is no fp32 number: blocks of zeros stay zeros, small values are
+    scaled by it exactly, others saturate."""
+    x = randn(70, 200, seed=3, dtype=TYPES[dtype])
+    x[:32] *= 2.0 ** -133 if f < 2.0 ** -128 else 2.0 ** -112
+    x[5, :64], x[60, :64], x[66:] = 0, 0, 0
+    x[8, 3], x[61, 190] = float("inf"), float("nan")
+    xd = x.cuda()
+    q, t = operand("nvfp4", 70, 200, f=f), operand("nvfp4", 200, 70, f=f)
+    t.factor = q.factor
+    mgt.mx4_quantize(xd, q, t)
+    check_bytes(q, np64(xd), f)
+    check_bytes(t, np64(xd).T, f)
+    for one in (q, t):
+        z = np64(xd) if one is q else np64(xd).T
+        for alone in (dict(q=one), dict(qt=one)):
+            src = xd if (one is q) == ("q" in alone) else xd.t().contiguous()
+            one.codes.fill_(0xCB)
+            one.scales.fill_(0xCB)
+            mgt.mx4_quantize(src, **alone)
+            check_bytes(one, z, f)
+
+
+@pytest.mark.parametrize("M", [6, 300])
+@pytest.mark.parametrize("f", [2.0 ** -149, 2.0 ** -130, 2.0 ** -110])
+def test_gated_product_with_a_tiny_factor(f, M):
+    """Its result's blocks are zeros where gate or up is, and vanish, fit or saturate elsewhere. The product
+    act(gate) * up is subnormal, off by half of 2^-149. The smallest blocks are near 2^-135. With f = 2^-130
+    their scale is 2^-8 and the first border between elements 2^-2 of it, 2^-140: half a unit is 2^-10 of
+    that. With f = 2^-149 all scales are 448 and the first border is 112 units: half a unit is 2^-7.8 of it."""
+    F, K, fx, fw = 150, 128, 2.0 ** -70, 2.0 ** -12
+    x, w = randn(M, K, seed=1, scale=2.0 ** -60), randn(512, K, seed=2, scale=2.0 ** -4)
+    x[1::3] = 0
+    x[2::3] *= 2.0 ** -6
+    w[256:] *= 2.0 ** -2
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    X, W = operand("nvfp4", M, K, x.cuda(), fx), operand("nvfp4", 512, K, w.cuda(), fw)
+    gate, up = (np64(values_of(X) @ values_of(W.rows_view(r, F)).T) for r in (0, 256))
+    a = operand("nvfp4", M, F, f=f)
+    mgt.gemm_mx4_gated(X, W, a, st)
+    assert (values_of(a)[1::3] == 0).all() and int(st) == 0
+    check_near(a, mx4.act(gate, "silu")[0] * up, f, 2.0 ** -7 if f == 2.0 ** -149 else 2.0 ** -9, most=0.2)
