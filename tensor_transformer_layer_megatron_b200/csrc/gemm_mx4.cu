@@ -1076,23 +1076,24 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   const int places = (two ? 2 : 1) * num_sms;
   // With one CTA per SM, how many clusters of a size are resident at once depends on how they fill
   // the GPU's processor groups (16 clusters of eight do not: 4096 x 100 x 4096 took 18.7 us with
-  // them, 11.0 without): the driver is asked, once per size and shape. With two per SM its answer
+  // them, 11.0 without): the driver is asked, once per device, size and shape. With two per SM its answer
   // is lower than what runs best.
-  static std::atomic<int> resident[17][9];  // clusters + 1, by bnq / 16 and size
+  static ResidentClusters resident;
   int split = ki < 8 ? ki : 8;
   for (; split > 1; --split) {
     if (tiles * split * 10 > 9 * places) continue;
     if (two) break;
-    int n = resident[bnq / 16][split].load(std::memory_order_relaxed);
-    if (n == 0) {
+    int dev = 0, n = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = resident.get(dev, bnq / 16, split, &n, [&](int* clusters) {
       cfg.gridDim = dim3((unsigned)split);
       cfg.numAttrs = 1;
       attr[0].val.clusterDim.x = (unsigned)split;
-      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-      if (e != cudaSuccess) return e;
-      resident[bnq / 16][split].store(++n, std::memory_order_relaxed);
-    }
-    if (tiles < n) break;
+      return cudaOccupancyMaxActiveClusters(clusters, kern, &cfg);
+    });
+    if (e != cudaSuccess) return e;
+    if (tiles <= n) break;
   }
   attr[0].val.clusterDim.x = (unsigned)split;
   cfg.numAttrs = 2;

@@ -24,6 +24,23 @@ struct SmemLimit {
   }
 };
 
+// How many clusters of a launch shape are resident at once, asked for once per device (devices may
+// differ in SMs and in how these are grouped). shape < kShapes, size (CTAs of a cluster) at most 8.
+struct ResidentClusters {
+  static constexpr int kDevices = 64, kShapes = 17;
+  std::atomic<int> known[kDevices][kShapes][9];  // + 1
+  // *n = the answer of ask(&n), a cudaError_t
+  template <typename Ask>
+  cudaError_t get(int dev, int shape, int size, int* n, Ask ask) {
+    std::atomic<int>* k = dev < kDevices ? &known[dev][shape][size] : nullptr;
+    *n = k ? k->load(std::memory_order_relaxed) - 1 : -1;
+    if (*n >= 0) return cudaSuccess;
+    const cudaError_t e = ask(n);
+    if (e == cudaSuccess && k) k->store(*n + 1, std::memory_order_relaxed);
+    return e;
+  }
+};
+
 // A 4-bit operand: packed codes (rows of ld / 2 bytes), scale tiles, leading dimension.
 struct Mx4Out {
   uint8_t* codes;

@@ -1,5 +1,8 @@
 """What the 4-bit operators refuse, before anything is launched (CPU: no GPU is touched)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -227,3 +230,20 @@ def test_an_operand_follows_its_factor_and_keeps_the_rest():
     m.factor = t
     m.factor = None
     assert m._c.factor is None
+
+
+def host_program(name, tmp_path):
+    """Compile tests/host/<name>.cu for the host and run it."""
+    nvcc = next((p for p in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc") if p and os.path.exists(p)), None)
+    if nvcc is None:
+        pytest.skip("nvcc not available")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "host", name + ".cu")
+    exe = str(tmp_path / name)
+    r = subprocess.run([nvcc, "-std=c++17", "-O1", "-o", exe, src], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
+
+
+def test_resident_clusters_are_kept_by_device(tmp_path):
+    host_program("mx4_clusters_check", tmp_path)
