@@ -128,7 +128,7 @@ __device__ __forceinline__ void gate_all(float (&v)[N], int act) {
 }
 
 constexpr int kStageK = 256;          // elements of K per stage: 128 bytes of a row
-constexpr int kPRows = 128;           // weight rows of a CTA's tile (per matrix)
+constexpr int kPRows = kSkinnyRows;   // weight rows of a CTA's tile (per matrix)
 constexpr int kPBytes = kPRows * 128;
 constexpr int kPrefetchStages = 8;    // stages fetched into L2 ahead: 128 KB a CTA
 
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(192)
   constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;  // scale tiles per stage and 128 rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int groups = g.bnq > 128 ? 2 : 1;  // 128-row groups of the tokens' scales
+  // 128-row groups of the tokens' scales
+  const int groups = !GATED && g.bnq > 128 ? 2 : 1;
   const int stage_bytes = NM * kPBytes + g.bnq * 128;
   const int sf_bytes = (NM + groups) * kTps * 512;
   uint8_t* sf = smem + g.stages * stage_bytes;
@@ -1005,31 +1006,10 @@ bool store_vec4(const void* p, long long ld, int esz) {
 
 template <int FMT, bool GATED>
 cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
-  constexpr int NM = GATED ? 2 : 1;
-  constexpr int kTps = kStageK / Mx4Fmt<FMT>::kTileCols;
-  const int most = GATED ? 128 : 256;
-  const int bnq = g.M < most ? (g.M + 15) & ~15 : most;
-  const int groups = bnq > 128 ? 2 : 1;
+  const SkinnyShape shape = skinny_shape(FMT == kNvfp4, GATED, g.M);
+  if (!shape.stages) return cudaErrorInvalidConfiguration;
+  const int bnq = shape.tokens;
   const int kp = (g.K + 127) & ~127, ki = (kp + kStageK - 1) / kStageK;
-  const int stage_bytes = NM * kPBytes + bnq * 128 + (NM + groups) * kTps * 512;
-  const int acc = NM * ((bnq + 31) & ~31);
-  const int sf_cols = (NM + groups) * kTps * 4;
-  // Stages: two CTAs per SM where each gets two at least, and as many as shared and tensor memory
-  // hold. The partial tile, which takes the stages' place, has to fit into their operands.
-  const int operand_bytes = NM * kPBytes + bnq * 128;
-  auto stages_in = [&](int bytes, int columns) {
-    int n = bytes / stage_bytes;
-    while (n > 0 && acc + n * sf_cols > columns) --n;
-    return n >= 2 && NM * bnq * kPRows * 4 <= n * operand_bytes ? n : 0;
-  };
-  const int half = 113 * 1024 - 2048, room = 227 * 1024 - 2048;
-  int stages = stages_in(half, 256);
-  const bool two = stages > 0;
-  if (!two) stages = stages_in(room, 512);
-  if (!stages) return cudaErrorInvalidConfiguration;
-  int cols = 32;
-  while (cols < acc + stages * sf_cols) cols *= 2;
-  const size_t smem = 1024 + (size_t)stages * stage_bytes + 16 * stages + 64;
 
   const int up0 = (g.N + 127) & ~127;  // first up row of a gated weight operand
   CUtensorMap tp, tp2, tq;
@@ -1039,7 +1019,7 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
     return cudaErrorInvalidValue;
   SkinnyArgs a = {};
   a.M = g.M; a.N = g.N; a.kp = kp;
-  a.bnq = bnq; a.stages = stages; a.tmem_cols = cols;
+  a.bnq = bnq; a.stages = shape.stages; a.tmem_cols = shape.tmem_cols;
   a.p_scales = g.B.scales;
   a.p2_scales = g.B.scales + (up0 / 128) * (g.B.ld / Mx4Fmt<FMT>::kTileCols) * 512;
   a.p_ld = g.B.ld;
@@ -1058,7 +1038,7 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)shape.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1073,7 +1053,7 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   // 20.3, four 10.1, eight 9.0.)
   const int tiles_p = (g.N + kPRows - 1) / kPRows, tiles_q = (g.M + bnq - 1) / bnq;
   const long long tiles = (long long)tiles_p * tiles_q;
-  const int places = (two ? 2 : 1) * num_sms;
+  const int places = (shape.two ? 2 : 1) * num_sms;
   // With one CTA per SM, how many clusters of a size are resident at once depends on how they fill
   // the GPU's processor groups (16 clusters of eight do not: 4096 x 100 x 4096 took 18.7 us with
   // them, 11.0 without): the driver is asked, once per device, size and shape. With two per SM its answer
@@ -1082,7 +1062,7 @@ cudaError_t launch_skinny(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
   int split = ki < 8 ? ki : 8;
   for (; split > 1; --split) {
     if (tiles * split * 10 > 9 * places) continue;
-    if (two) break;
+    if (GATED || shape.two) break;
     int dev = 0, n = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1172,7 +1152,7 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
 // 6144; with three 18.0 against 19.1 at 512 x 2560 x 11008 and 16.4 against 15.6 at K = 8192; with two
 // 32.8 against 36.1 at 1024 x 2048 x 24576 and 22.7 against 20.7 at K = 12288.
 bool few_rows(const Mx4Gemm& g, int num_sms) {
-  if (g.gated) return g.M <= 64;
+  if (g.gated) return g.M <= kSkinnyGatedTokens;
   if (g.M <= 96) return true;
   const long long tiles = (long long)((g.M + 255) / 256) * ((g.N + 127) / 128);
   const int ki = (g.K + kStageK - 1) / kStageK;

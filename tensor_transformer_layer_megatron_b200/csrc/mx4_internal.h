@@ -41,6 +41,54 @@ struct ResidentClusters {
   }
 };
 
+// Launch shape of the few-row product (mx4_skinny_kernel in gemm_mx4.cu) for M tokens.
+constexpr int kSkinnyRows = 128;        // weight rows of a CTA's tile (per matrix)
+constexpr int kSkinnyTokens = 256;      // most tokens of a tile
+constexpr int kSkinnyGatedTokens = 64;  // the same for a gated product, and its most tokens at all
+struct SkinnyShape {
+  int tokens;       // of a tile: a multiple of 16
+  int stages;       // 256 elements of the summed axis each; 0: no shape fits
+  int stage_bytes;  // operands and scales
+  int tmem_cols;    // allocated tensor-memory columns
+  int smem;         // dynamic shared memory
+  bool two;         // two CTAs per SM
+};
+constexpr SkinnyShape skinny_shape(bool nvfp4, bool gated, int M) {
+  SkinnyShape r = {};
+  const int most = gated ? kSkinnyGatedTokens : kSkinnyTokens;
+  const int matrices = gated ? 2 : 1, scale_tiles = nvfp4 ? 4 : 2;  // of a stage and 128 rows
+  r.tokens = M < most ? (M + 15) & ~15 : most;
+  const int groups = r.tokens > 128 ? 2 : 1;  // 128-row groups of the tokens' scales
+  const int operand_bytes = (matrices * kSkinnyRows + r.tokens) * 128;
+  const int scales = (matrices + groups) * scale_tiles;
+  r.stage_bytes = operand_bytes + scales * 512;
+  const int acc = matrices * ((r.tokens + 31) & ~31);
+  // Two CTAs per SM where each gets two stages at least, and as many stages as shared and tensor
+  // memory hold. The partial tile, which takes the stages' place, has to fit into their operands.
+  for (int per_sm = 2; per_sm > 0 && !r.stages; --per_sm) {
+    const int bytes = (per_sm == 2 ? 113 : 227) * 1024 - 2048, columns = 512 / per_sm;
+    int n = bytes / r.stage_bytes;
+    while (n > 0 && acc + n * scales * 4 > columns) --n;
+    if (n >= 2 && matrices * r.tokens * kSkinnyRows * 4 <= n * operand_bytes) r.stages = n;
+    r.two = per_sm == 2;
+  }
+  r.tmem_cols = 32;
+  while (r.tmem_cols < acc + r.stages * scales * 4) r.tmem_cols *= 2;
+  r.smem = 1024 + r.stages * (r.stage_bytes + 16) + 64;
+  return r;
+}
+// Every number of tokens has a shape, and a gated product shares its SM (its kernel has no other form).
+constexpr bool skinny_shapes_fit() {
+  for (int M = 1; M <= kSkinnyTokens; ++M)
+    for (int k = 0; k < 4; ++k) {
+      if ((k & 1) && M > kSkinnyGatedTokens) continue;
+      const SkinnyShape s = skinny_shape(k & 2, k & 1, M);
+      if (!s.stages || ((k & 1) && !s.two)) return false;
+    }
+  return true;
+}
+static_assert(skinny_shapes_fit(), "a token count without a launch shape");
+
 // A 4-bit operand: packed codes (rows of ld / 2 bytes), scale tiles, leading dimension.
 struct Mx4Out {
   uint8_t* codes;

@@ -789,3 +789,36 @@ def test_gated_product_with_a_tiny_factor(f, M):
     mgt.gemm_mx4_gated(X, W, a, st)
     assert (values_of(a)[1::3] == 0).all() and int(st) == 0
     check_near(a, mx4.act(gate, "silu")[0] * up, f, 2.0 ** -7 if f == 2.0 ** -149 else 2.0 ** -9, most=0.2)
+
+
+def levels(rows, cols, seed, scale=1.0):
+    """Random elements times a power of two; every block holds a 6, so that its scale is that power."""
+    g = torch.Generator("cpu").manual_seed(seed)
+    x = torch.tensor(mx4.LEVELS)[torch.randint(8, (rows, cols), generator=g)]
+    x[:, ::16] = 6
+    x = x * (2.0 * torch.randint(2, (rows, cols), generator=g) - 1)
+    return (x * scale).float()
+
+
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 31, 32, 47, 48, 49, 63, 64, 65, 80])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gated_product_at_every_token_tile(fmt, M):
+    """Every tile of the few-row kernel's gated form and the first row counts of the other one, sums split
+    over eight CTAs. All sums are multiples of 2^-9 below 2^12, so any order gives them exactly: u is
+    their rounding, and `a` is off by the activation's 2^-21 + |z| 2^-24 (|z| < 32) and one product."""
+    F, K = 300, 2200
+    x, w = levels(M, K, M), levels(768, K, 1000 + M, 2.0 ** -7)
+    X, W = operand(fmt, M, K, x.cuda(), fill=0xFF), operand(fmt, 768, K, w.cuda())
+    assert torch.equal(values_of(X).float(), x.cuda()) and torch.equal(values_of(W).float(), w.cuda())
+    gate, up = (x.double() @ w[r:r + F].double().T for r in (0, 384))
+    assert gate.abs().max() < 32
+    f = 1.0 if fmt == "mxfp4" else 2.0 ** -4
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for pad in (0, 3):  # aligned rows of u and others
+        u = torch.full((M + 1, 2 * F + pad), 3.0, dtype=torch.bfloat16, device="cuda")
+        a = operand(fmt, M, F, f=f)
+        mgt.gemm_mx4_gated(X, W, a, st, u=u[:M, :2 * F])
+        assert torch.equal(u[:M, :2 * F].cpu(), torch.cat([gate, up], 1).bfloat16())
+        assert (u[M] == 3).all() and (u[:, 2 * F:] == 3).all()
+        check_near(a, mx4.act(gate.numpy(), "silu")[0] * up.numpy(), f, 2.0 ** -18, most=0.001)
+    assert int(st) == 0

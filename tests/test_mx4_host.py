@@ -247,3 +247,7 @@ def host_program(name, tmp_path):
 
 def test_resident_clusters_are_kept_by_device(tmp_path):
     host_program("mx4_clusters_check", tmp_path)
+
+
+def test_launch_shapes_of_the_few_row_product(tmp_path):
+    host_program("mx4_shapes_check", tmp_path)
