@@ -171,11 +171,16 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 
 // Programmatic dependent launch. A kernel launched with programmatic stream serialization
-// (launch_kernel) may be scheduled once every CTA of the previous kernel of its stream has
-// exited, before that grid has completed and flushed its writes; every thread calls
-// grid_dependency_wait() after its shared-memory and TMEM set-up and before its first
-// global-memory access, which returns once that kernel has completed and its writes are
-// visible. No kernel triggers its dependents earlier than its own exit: CTAs that were
+// (launch_kernel) may be scheduled before the previous kernel of its stream has completed and
+// flushed its writes: once every CTA of that kernel has exited, or, behind a kernel that lets its
+// dependents go at its start (launch_dependents: the 4-bit quantisers and few-row products), while
+// all of it still runs. So every thread calls grid_dependency_wait() after its shared-memory and
+// TMEM set-up and before it reads or writes global memory, on every path that leads to the
+// kernel's end; the call returns once the previous kernel has completed and its writes are
+// visible. Before it only tensor-map descriptors and prefetches into L2 are allowed. A kernel
+// that waits for nothing could complete before its predecessor has, and its successors, which
+// wait for it alone, would run into that predecessor's writes.
+// The layer's kernels do not let their dependents go before their own exit: CTAs that were
 // resident early would hold SMs idle that the backward's second stream fills. Without a
 // programmatic predecessor the wait returns at once.
 __device__ __forceinline__ void grid_dependency_wait() {
