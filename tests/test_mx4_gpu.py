@@ -822,3 +822,74 @@ def test_gated_product_at_every_token_tile(fmt, M):
         assert (u[M] == 3).all() and (u[:, 2 * F:] == 3).all()
         check_near(a, mx4.act(gate.numpy(), "silu")[0] * up.numpy(), f, 2.0 ** -18, most=0.001)
     assert int(st) == 0
+
+
+def decoded(q, r0, r1):
+    """Rows r0 .. r1 - 1 (r0 a multiple of 128) of an operand of factor 1, by the layout's definition, float64."""
+    n, code = mx4.BLOCK[q.fmt], q.codes[r0:r1]
+    table = torch.tensor([*mx4.LEVELS, *-mx4.LEVELS], device="cuda")
+    v = torch.stack([code & 15, code >> 4], 2).view(r1 - r0, -1)
+    tiles = q.scales.view(-1, q.ld // (4 * n), 32, 4, 4)[r0 // 128:(r1 + 127) // 128]
+    byte = tiles.permute(0, 3, 2, 1, 4).reshape(-1, q.ld // n)[:r1 - r0].double()
+    s = 2.0 ** (byte - 127) if q.fmt == "mxfp4" else 2.0 ** ((byte - 0x38) / 8)  # (powers of two only)
+    return (table[v.int()].view(r1 - r0, -1, n) * s.unsqueeze(2)).view(r1 - r0, -1)[:, :q.cols]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_products_beyond_32_bit_offsets_to_the_bit(fmt):
+    """70144 x 65500 elements (2.3 GB of codes) as either operand and as a gated block's weights, every result
+    against float64. Elements are random codes, scales 1 or 2: products are multiples of 1/4 up to
+    144, sums of them far below 2^22, so that fp32 adds them exactly in any order."""
+    F, C, M = 35000, 65500, 300
+    P = (F + 127) // 128 * 128
+    gen = torch.Generator("cuda").manual_seed(11)
+
+    def filled(rows):
+        q = operand(fmt, rows, C)
+        q.codes.random_(0, 256, generator=gen)
+        q.codes[:, C // 2:] = 0
+        one, two = (127, 128) if fmt == "mxfp4" else (0x38, 0x40)
+        q.scales.random_(0, 2, generator=gen).mul_(two - one).add_(one)
+        return q
+
+    q, v = filled(2 * P), filled(M)
+    ref = torch.empty(M, 2 * P, dtype=torch.float64, device="cuda")
+    few = decoded(v, 0, M)
+    for r0 in range(0, 2 * P, 4096):
+        r1 = min(2 * P, r0 + 4096)
+        ref[:, r0:r1] = few @ decoded(q, r0, r1).t()
+    assert float(ref.abs().max()) < 2.0 ** 20
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for rows in (33, M):  # few rows, and tiles of 256
+        V = v.rows_view(0, rows)
+        out = torch.empty(rows, 2 * P, device="cuda")
+        mgt.gemm_mx4(V, q, out, st)
+        assert torch.equal(out.double(), ref[:rows])
+        out = torch.empty(2 * P, rows, device="cuda")
+        mgt.gemm_mx4(q, V, out, st)
+        assert torch.equal(out.double(), ref[:rows].t())
+        a, u = operand(fmt, rows, F, f=2.0 ** 10), torch.empty(rows, 2 * F, dtype=torch.bfloat16, device="cuda")
+        mgt.gemm_mx4_gated(V, q, a, st, u=u)
+        gate, up = ref[:rows, :F], ref[:rows, P:P + F]
+        assert torch.equal(u, torch.cat([gate, up], 1).bfloat16())
+        # act(gate) is gate or nothing at this size; two roundings of 2^-24 and the activation's 2^-21
+        some = slice(0, None, 7)  # (every seventh row: the oracle runs on the CPU)
+        check_near(operand_rows(a, some), mx4.act(np64(gate[some]), "silu")[0] * np64(up[some]),
+                   1.0 if fmt == "mxfp4" else 2.0 ** 10, 2.0 ** -18, most=0.001)
+    assert int(st) == 0
+
+
+def operand_rows(q, rows):
+    """Some rows of an operand, copied into one of their own by way of their values (exact)."""
+    y = values_of(q)[rows].float()
+    f = float(q.factor[1]) if q.fmt == "nvfp4" else 1.0
+    c = operand(q.fmt, *y.shape, f=f)
+    n = mx4.BLOCK[q.fmt]
+    k = torch.arange(q.rows, device="cuda")[rows]
+    c.codes.copy_(q.codes[rows])
+    at = lambda r, b: ((r // 128) * (q.ld // (4 * n)) + b // 4) * 512 + 16 * (r % 32) + 4 * (r % 128 // 32) + b % 4  # noqa: E731
+    b = torch.arange(q.ld // n, device="cuda").view(1, -1)
+    to = torch.arange(len(k), device="cuda").view(-1, 1)
+    c.scales[at(to, b)] = q.scales[at(k.view(-1, 1), b)]
+    assert torch.equal(values_of(c).float(), y)
+    return c
