@@ -893,3 +893,83 @@ def operand_rows(q, rows):
     c.scales[at(to, b)] = q.scales[at(k.view(-1, 1), b)]
     assert torch.equal(values_of(c).float(), y)
     return c
+
+
+def check_every(q, exact, err, f=1.0):
+    """Each element of q is one that a number within err (elementwise, absolute) of exact rounds to: for the
+    scale of its block from the smallest or the largest such maximum, between the roundings of the
+    ends."""
+    got, n = np64(values_of(q)), mx4.BLOCK[q.fmt]
+    low, high = np.maximum(np.abs(exact) - err, 0), np.abs(exact) + err
+    fits = np.zeros(got.shape, bool)
+    for end in (low, high):
+        byte = mx4.quantize(end, q.fmt, f)[1].astype(np.float64)
+        if q.fmt == "mxfp4":
+            scale = 2.0 ** (byte - 127)
+        else:
+            e, m = np.floor(byte / 8), byte % 8
+            scale = np.where(e > 0, (8 + m) * 2.0 ** (e - 10), m * 2.0 ** -9) * f
+        scale = np.repeat(scale, n, 1)[:, :got.shape[1]]
+        least, most = (mx4.LEVELS[mx4.e2m1_round(np.where(scale > 0, v / np.where(scale > 0, scale, 1), 0))] * scale
+                       for v in (low, high))
+        sign = np.where(np.abs(exact) > err, np.sign(exact), np.sign(got))
+        fits |= (np.abs(got) >= least) & (np.abs(got) <= most) & ((got == 0) | (np.sign(got) == sign))
+    assert fits.all(), np.argwhere(~fits)[:4]
+
+
+def act_errors(z, act):
+    """(h, dh, error of h, error of dh) of the kernels' fp32 activations, from their formulas. e: the
+    relative error of sigmoid, Phi or the tanh form's sigmoid."""
+    h, dh = mx4.act(z, act)
+    a = np.abs(z)
+    if act == "silu":  # the exponent's product, ex2.approx, rcp.approx: 2^-21 + |z| 2^-24
+        s = 1 / (1 + np.exp(-z))
+        e = 2.0 ** -20.5 + a * 2.0 ** -24
+        # s (1 + z (1 - s)): s once for itself, once in 1 - s, and roundings of terms up to 1 + |z|
+        return h, dh, np.abs(h) * e, s * ((1 + a * (1 - s)) * e + a * s * e + (1 + a) * 2.0 ** -23)
+    if act == "gelu":  # arguments with 2^-23 of z^2 / 2 as error; erfcf within four units, expf two
+        c, pdf = np.where(z == 0, 0.5, h / np.where(z == 0, 1, z)), np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+        e = 2.0 ** -20.5 + z * z * 2.0 ** -23
+        return h, dh, np.abs(h) * e, (c + a * pdf) * e
+    w = 2 * np.sqrt(2 / np.pi) * a * (1 + 0.044715 * z * z)
+    s, inner = 1 / (1 + np.exp(-np.sign(z) * w)), 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * z * z)
+    # the exponent is off by four roundings of w + 1.4; 1 / (1 + E) moves by s (1 - s) of that
+    e = 2.0 ** -21 + (w + 2) * 2.0 ** -22 * (1 - s)
+    return h, dh, np.abs(h) * e, s * ((1 + a * (1 - s) * inner) * e + a * inner * (s * e + 2.0 ** -23) + 2.0 ** -23)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,F", [(130, 260), (40, 1000)])
+def test_gated_backward_to_the_last_step(fmt, act, M, F):
+    """Every element, the ones next to a border too: products of three bf16 numbers or two and an
+    activation round twice more in fp32."""
+    da, u = randn(M, F, seed=1, scale=1e-3, dtype=torch.bfloat16), randn(M, 2 * F, seed=2, scale=2.0, dtype=torch.bfloat16)
+    P, d = (F + 127) // 128 * 128, np64(da)
+    z, up = np64(u[:, :F]), np64(u[:, F:])
+    h, dh, eh, edh = act_errors(z, act)
+    fd, fa = (1.0, 1.0) if fmt == "mxfp4" else (2.0 ** -18, 2.0 ** -8)
+    du, dut, at = operand(fmt, M, 2 * P, f=fd), operand(fmt, 2 * P, M, f=fd), operand(fmt, F, M, f=fa)
+    mgt.mx4_gated_bwd(da.cuda(), u.cuda(), du, dut, at, act=act)
+    for k, (exact, err) in enumerate(((d * up * dh, np.abs(d * up) * edh), (d * h, np.abs(d) * eh))):
+        err = err + np.abs(exact) * 2.0 ** -22
+        check_every(du.part(0, M, k * P, F), exact, err, fd)
+        check_every(dut.rows_view(k * P, F), exact.T, err.T, fd)
+    check_every(at, (h * up).T, (np.abs(up) * eh + np.abs(h * up) * 2.0 ** -22).T, fa)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [3, 48, 300])
+def test_gated_product_to_the_last_step(fmt, act, M):
+    """Every element of the quantised result, on gates and ups that any order of sums gives exactly."""
+    F, K = 300, 600
+    x, w = levels(M, K, M), levels(768, K, 1000 + M, 2.0 ** -7)
+    X, W = operand(fmt, M, K, x.cuda()), operand(fmt, 768, K, w.cuda())
+    gate, up = ((x.double() @ w[r:r + F].double().T).numpy() for r in (0, 384))
+    f = 1.0 if fmt == "mxfp4" else 2.0 ** -5
+    a, st = operand(fmt, M, F, f=f), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mgt.gemm_mx4_gated(X, W, a, st, act=act)
+    h, _, eh, _ = act_errors(gate, act)
+    check_every(a, h * up, np.abs(up) * eh + np.abs(h * up) * 2.0 ** -23, f)
+    assert int(st) == 0
