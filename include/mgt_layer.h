@@ -277,8 +277,9 @@ mgt_status mgt_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* A, int64
  *
  * All calls are asynchronous on `stream`, allocate nothing, keep nothing and check their arguments
  * before they launch (MGT_EINVAL for shapes that do not fit together and missing pointers,
- * MGT_EUNSUPPORTED for types and alignments). Outputs may not overlap inputs. Results do not
- * depend on timing or order. They may be captured into a graph. */
+ * MGT_EUNSUPPORTED for types and alignments). Outputs may not overlap inputs or one another (two
+ * operands that start at one address are refused). Results do not depend on timing or order. They
+ * may be captured into a graph. */
 typedef enum mgt_mx4_format { MGT_MXFP4 = 0, MGT_NVFP4 = 1 } mgt_mx4_format;
 typedef enum mgt_act { MGT_ACT_SILU = 0, MGT_ACT_GELU = 1, MGT_ACT_GELU_TANH = 2 } mgt_act;
 

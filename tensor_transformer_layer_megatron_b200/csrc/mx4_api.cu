@@ -29,6 +29,11 @@ mgt_status check(const mgt_mx4* q) {
   return MGT_OK;
 }
 
+// Two results in one place (parts of one buffer are fine).
+bool same_place(const mgt_mx4* a, const mgt_mx4* b) {
+  return a && b && (a->codes == b->codes || a->scales == b->scales);
+}
+
 bool dtype_ok(int32_t d) { return d == MGT_F32 || d == MGT_BF16; }
 unsigned esz(int32_t d) { return d == MGT_F32 ? 4 : 2; }
 
@@ -100,6 +105,7 @@ mgt_status mgt_mx4_quantize(int32_t dtype, const void* x, int64_t ldx, const mgt
   const int rows = q ? q->rows : qt->cols, cols = q ? q->cols : qt->rows;
   if (ldx < cols) return MGT_EINVAL;
   if (!dtype_ok(dtype) || !aligned(x, esz(dtype))) return MGT_EUNSUPPORTED;
+  if (same_place(q, qt)) return MGT_EINVAL;
   MX4_SMS(n);
   (void)n;
   return status_of(launch_mx4_quantize(q ? q->format : qt->format, dtype == MGT_BF16, rows, cols,
@@ -150,6 +156,7 @@ mgt_status mgt_gemm_mx4_gated(const mgt_mx4* X, const mgt_mx4* W, int32_t act, c
       X->rows != a->rows || W->rows != 2 * up128(a->cols) || (u && ldu < 2 * (int64_t)a->cols))
     return MGT_EINVAL;
   if (!aligned(u, 2) || !aligned(status, 4)) return MGT_EUNSUPPORTED;
+  if (same_place(a, X) || same_place(a, W)) return MGT_EINVAL;
   MX4_SMS(n);
   Mx4Gemm g = {};
   g.fmt = X->format;
@@ -183,6 +190,7 @@ mgt_status mgt_mx4_gated_bwd(int32_t act, int32_t rows, int32_t ffn, const void*
     return MGT_EINVAL;
   if (act < MGT_ACT_SILU || act > MGT_ACT_GELU_TANH) return MGT_EUNSUPPORTED;
   if (!aligned(da, 2) || !aligned(u, 2)) return MGT_EUNSUPPORTED;
+  if (same_place(du, dut) || same_place(du, at) || same_place(dut, at)) return MGT_EINVAL;
   MX4_SMS(n);
   (void)n;
   return status_of(launch_mx4_gated_bwd(

@@ -125,6 +125,25 @@ def test_gated_refusals(lib):
     assert bwd(da=P + 1) == EUNSUPPORTED
 
 
+def test_two_results_in_one_place_are_refused(lib):
+    q = operand(128, 128, codes=P)
+    for other in (dict(codes=P), dict(scales=P)):  # (codes and scales of `operand` lie at P)
+        t = operand(128, 128, **{"codes": P + 65536, "scales": P + 65536, **other})
+        assert lib.mgt_mx4_quantize(1, P, 128, ref(q), ref(t), None) == EINVAL
+    far = lambda k, r, c: operand(r, c, codes=P + 65536 * k, scales=P + 65536 * k)  # noqa: E731
+    three = [far(0, 128, 256), far(1, 256, 128), far(2, 128, 128)]
+    for k in range(3):
+        for name in ("codes", "scales"):
+            bad = list(three)
+            bad[k] = operand(bad[k].rows, bad[k].cols, codes=bad[k].codes, scales=bad[k].scales)
+            setattr(bad[k], name, getattr(bad[(k + 1) % 3], name))
+            assert lib.mgt_mx4_gated_bwd(0, 128, 128, P, 128, P, 256, *map(ref, bad), None) == EINVAL
+    x, w, a = far(0, 4, 100), far(1, 512, 100), far(2, 4, 200)
+    for other in (x, w):
+        b = operand(4, 200, codes=a.codes, scales=other.scales)
+        assert lib.mgt_gemm_mx4_gated(ref(x), ref(w), 0, ref(b), None, 0, P, None) == EINVAL
+
+
 def test_python_operands():
     mk = lambda *a, **k: mgt.Mx4(*a, device="cpu", **k)  # noqa: E731
     q = mk("nvfp4", 300, 200)
