@@ -973,3 +973,93 @@ def test_gated_product_to_the_last_step(fmt, act, M):
     h, _, eh, _ = act_errors(gate, act)
     check_every(a, h * up, np.abs(up) * eh + np.abs(h * up) * 2.0 ** -23, f)
     assert int(st) == 0
+
+
+FIRST_CALLS = """
+import threading, torch
+import tensor_transformer_layer_megatron_b200 as mgt
+M, K, F, fmt = 40, 1024, 300, {fmt!r}
+dev = dict(device="cuda")
+gen = torch.Generator("cuda").manual_seed(1)
+
+class Run:
+    def __init__(self, seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.x = torch.randn(M, K, generator=g, **dev).bfloat16()
+        self.w = torch.randn(768, K, generator=g, **dev) * 0.05
+        self.q, self.W, self.a, self.at = (mgt.Mx4(fmt, *n) for n in ((M, K), (768, K), (M, F), (F, M)))
+        self.du = mgt.Mx4(fmt, M, 768)
+        self.u, self.y = torch.empty(M, 2 * F, dtype=torch.bfloat16, **dev), torch.empty(M, F, **dev)
+        self.big = torch.empty(768, 768, **dev)
+        self.st = torch.zeros(1, dtype=torch.int32, **dev)
+
+    def go(self, stream=None):
+        if fmt == "nvfp4":
+            mgt.mx4_tensor_factor(self.x, self.q.factor, stream)
+            mgt.mx4_tensor_factor(self.w, self.W.factor, stream)
+        mgt.mx4_quantize(self.x, self.q, stream=stream)
+        mgt.mx4_quantize(self.w, self.W, stream=stream)
+        mgt.gemm_mx4_gated(self.q, self.W, self.a, self.st, u=self.u, stream=stream)
+        mgt.mx4_dequantize(self.a, self.y, stream=stream)
+        mgt.mx4_gated_bwd(self.y.bfloat16() if stream is None else self.u[:, :F], self.u, self.du, None, self.at, stream=stream)
+        mgt.gemm_mx4(self.W, self.W, self.big, self.st, stream=stream)
+
+    def out(self):
+        return [t.clone() for t in (self.u, self.y, self.big, self.a.codes, self.du.codes, self.at.codes)]
+"""
+
+
+def run_python(code):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_first_calls_of_a_process_may_be_captured(fmt):
+    """Nothing has to run eagerly before: a process whose first calls go into a graph."""
+    run_python(FIRST_CALLS.format(fmt=fmt) + """
+r = Run(1)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    r.go()
+g.replay()
+torch.cuda.synchronize()
+got = r.out()
+r.go()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, r.out())) and int(r.st) == 0
+print("ok")
+""")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_first_calls_from_two_threads(fmt):
+    """Two threads that begin at once, on a stream each."""
+    run_python(FIRST_CALLS.format(fmt=fmt) + """
+runs, streams = [Run(1), Run(2)], [torch.cuda.Stream() for _ in range(2)]
+torch.cuda.synchronize()
+errors, gate = [], threading.Barrier(2)
+def work(r, s):
+    try:
+        gate.wait()
+        for _ in range(20):
+            r.go(s)
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=work, args=a) for a in zip(runs, streams)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+got = [r.out() for r in runs]
+for r, was, s in zip(runs, got, streams):
+    r.go(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(was, r.out())) and int(r.st) == 0
+print("ok")
+""")
