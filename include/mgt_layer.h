@@ -259,7 +259,7 @@ mgt_status mgt_gemm_fp8(int32_t M, int32_t N, int32_t K, const uint8_t* A, int64
  *              scale) may be any positive number, and a power of two keeps every rounding
  *              decision exact.
  *
- * mgt_mx4: one operand of `rows` by `cols`, each at least one.
+ * mgt_mx4: one operand of `rows` by `cols`, each at least one and at most 2^30.
  *   codes    rows of ld / 2 bytes, two elements to a byte, the even column in the low half.
  *            Columns from cols up to the next multiple of 128 are read by the products and hold
  *            zeros, with any scale but NaN (every call that writes an operand writes them).
@@ -327,7 +327,8 @@ mgt_status mgt_gemm_mx4(const mgt_mx4* A, const mgt_mx4* B, void* C, int32_t c_d
  * 128, W->rows = 2 P (rows between are not read into any result). gate, up and the activation
  * stay in fp32; a ([X->rows][ffn]) leaves quantised, ready for the product with W2. u (optional,
  * bf16, row stride ldu >= 2 ffn) receives [gate | up] for the backward. act: mgt_act, GeLU exact
- * or tanh. For MGT_NVFP4 a->factor is an input: a kept scale. */
+ * or tanh. For MGT_NVFP4 a->factor is an input, a kept scale; the result's maximum is not reported,
+ * and values beyond 2688 f saturate. */
 mgt_status mgt_gemm_mx4_gated(const mgt_mx4* X, const mgt_mx4* W, int32_t act, const mgt_mx4* a,
                               void* u, int64_t ldu, int32_t* status, void* stream);
 
@@ -337,7 +338,8 @@ mgt_status mgt_gemm_mx4_gated(const mgt_mx4* X, const mgt_mx4* W, int32_t act, c
  * du  [rows][2 P]: dgate from column 0, dup from column P (zeros behind each): with W1^T ([hidden][2 P],
  *     quantised along its rows) laid out alike, dX = du (W1^T)^T is one mgt_gemm_mx4;
  * dut [2 P][rows]: dgate^T from row 0, dup^T from row P: the weight gradients of gate and up;
- * at  [ffn][rows]: a^T, for dW2. Any of them may be NULL, not all. MGT_NVFP4: factors are inputs. */
+ * at  [ffn][rows]: a^T, for dW2. Any of them may be NULL, not all. MGT_NVFP4: each has a factor of its
+ *     own, an input; the maxima are not reported, and values beyond 2688 f saturate. */
 mgt_status mgt_mx4_gated_bwd(int32_t act, int32_t rows, int32_t ffn, const void* da, int64_t ldda,
                              const void* u, int64_t ldu, const mgt_mx4* du, const mgt_mx4* dut,
                              const mgt_mx4* at, void* stream);

@@ -141,8 +141,10 @@ constexpr int kPrefetchStages = 8;    // stages fetched into L2 ahead: 128 KB a 
 //
 // Bound by the weights' bytes and, at these sizes, by what comes before and after them (launch,
 // first loads, sum over the cluster): one token, mxfp4, 12288 x 4096 7.8 us with its launch (26.7
-// MB, 3.4 TB/s), 4096 x 11008 7.6 us, 49152 x 4096 28 us; gated 2 x 11008 x 4096 11.1 us (nvfp4
-// 13.1).
+// MB, 3.4 TB/s; nvfp4 8.5), 4096 x 11008 7.5; gated 2 x 11008 x 4096 11.1 us, any activation (nvfp4
+// 12.9); 60 tokens with u kept 16.4 / 17.8; 90 tokens x 12288 x 4096 12.2 / 13.0. More tiles than
+// places, 49152 x 4096: 384 CTAs on 296 places are 1.3 rounds, of which the second fills 30 % of
+// the GPU: 28 us alone, 24 in a row of such calls, where the next call's weights are on their way.
 struct SkinnyArgs {
   int M, N, kp;                 // tokens, weight rows (per matrix), K rounded up to 128
   int bnq, stages, tmem_cols;
@@ -465,8 +467,11 @@ __global__ void __launch_bounds__(192)
 //
 // Bound by the tensor core and the shared memory that feeds it: a stage of 256 elements takes 650
 // to 710 cycles where its products alone take 512, and the hand-over between tiles about 1,500. 8192
-// x 24576 x 6144 mxfp4 457 us (5.4 PFLOP/s), nvfp4 500; 2048 x 12288 x 4096 57 / 62 us, 12288 x 4096
-// x 2048 into fp32 66; gated 2048 x 2 * 11008 x 4096 74 / 80 us, with u kept 83 / 90.
+// x 24576 x 6144 mxfp4 451 us (5.5 PFLOP/s), nvfp4 477; 2048 x 12288 x 4096 47 / 49 us, 12288 x 4096
+// x 2048 into fp32 61 / 66; gated 2048 x 2 * 11008 x 4096 silu 73 / 80 us, with u kept 82 / 89, gelu
+// 92 / 99 (99 / 105), tanh gelu 86 / 105 (95 / 113). These are runs of a millisecond; after seconds of
+// them the power cap holds the clock at 1.5 to 1.75 GHz and they take 8 to 17 % more (530 / 557, 55
+// / 57, 69 / 76, gated silu 86 / 94).
 struct PairArgs {
   int M, N, kp;
   int num_m, num_n, m_fast;
@@ -1141,7 +1146,7 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
 }
 
 // Whether the weights-as-rows kernel is the faster one (times with the quantisation of the rows,
-// mxfp4). It passes over the weights once per 128 or 256 rows and splits the sum; the pairs'
+// mxfp4). It passes over the weights once per 64 or 256 rows and splits the sum; the pairs'
 // tiles hold 256 rows. N x K = 12288 x 4096: 96 rows 15.0 us against 15.3, 128 rows 16.4 against
 // 15.4; gated 11008 x 4096: 64 rows 18.9 against 22.3, 96 rows 25.8 against 22.5. Where the sum is
 // long and the pairs' tiles leave most SMs idle the split wins further up: 4096 x 11008, 128 rows
@@ -1150,7 +1155,10 @@ cudaError_t launch_pair(const Mx4Gemm& g, int num_sms, cudaStream_t s) {
 // with six or more from 20 stages up (512 x 512 x 8192 10.3 against 15.2, 1000 x 128 x 16384 11.6
 // against 25.6); with four 14.6 against 18.9 at 768 x 1024 x 11008 and 13.4 against 12.8 at 512 x 2048 x
 // 6144; with three 18.0 against 19.1 at 512 x 2560 x 11008 and 16.4 against 15.6 at K = 8192; with two
-// 32.8 against 36.1 at 1024 x 2048 x 24576 and 22.7 against 20.7 at K = 12288.
+// 32.8 against 36.1 at 1024 x 2048 x 24576 and 22.7 against 20.7 at K = 12288. All crossings were
+// measured with mxfp4 and serve nvfp4 too, whose kernels take 4 to 15 % longer on both sides; the
+// gated one at this one width and sum. A gated product of more than 64 rows is never split, so few
+// tiles with a long sum (128 rows, 1024 outputs, K = 6144: 8 tiles) leave most pairs idle.
 bool few_rows(const Mx4Gemm& g, int num_sms) {
   if (g.gated) return g.M <= kSkinnyGatedTokens;
   if (g.M <= 96) return true;

@@ -159,7 +159,9 @@ struct Walk {
 // atomic maximum on the bits of out[0] (order free); the last block to arrive, counted in
 // out[1], writes f over the count. Both words are zeroed by a launch before, of one thread:
 // chained programmatically the two take 2.9 us for one row, with a memory set in its place 6.2.
-// Bound by HBM: 4096 x 11008 fp32 29 us (6.2 TB/s), 2048 x 4096 bf16 6.4 us. 256 threads with
+// Bound by HBM: 4096 x 11008 fp32 29 us (6.2 TB/s), 8192 x 24576 bf16 61 us (6.6), 2048 x 4096
+// bf16 6.4 us; rows that do not start on 16 bytes are read by words, 4096 x 11007 fp32 48 us, 8192
+// x 24575 bf16 84, 2048 x 4095 bf16 9.9. 256 threads with
 // four loads in flight, up to eight blocks per SM: no other shape tried was faster anywhere.
 __global__ void mx4_zero2_kernel(float* out) {
   launch_dependents();
@@ -226,11 +228,12 @@ __global__ void __launch_bounds__(256) mx4_factor_kernel(int rows, int cols, con
 // four (gated: four or eight) lanes that share it, along either direction: the transposed operand
 // needs no trip through shared memory, and a lane has eight loads in flight.
 //
-// Times (mxfp4 / nvfp4): bf16 along the rows 2048 x 4096 6.4 / 8.6 us, 8192 x 6144 26 / 34 us
+// Times (mxfp4 / nvfp4): bf16 along the rows 2048 x 4096 6.4 / 8.7 us, 8192 x 6144 26 / 34 us
 // (4.8 TB/s / 3.7); bf16 both ways 2048 x 12288 22 / 27 us; fp32 both ways 4096 x 11008 48 / 49 us
 // (4.8 TB/s). What bounds it is HBM for fp32 and, for bf16 and for nvfp4's quotients, the integer
 // and fp32 instructions per element (both ways: 59 % of the ALU's peak, 2.4 instructions a clock
-// and SM). Rows that do not start on 16 bytes are read by words: 10.0 / 14.2 us for 2048 x 4096.
+// and SM). Rows that do not start on 16 bytes are read by words: 2048 x 4095 bf16 9.4 / 13.9 us, with
+// rows of 4101 in memory 2048 x 4096 10.0 / 14.2, fp32 both ways 4096 x 11007 64 / 65.
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 128;
 
@@ -548,7 +551,8 @@ __global__ void __launch_bounds__(kTileThreads, FMT == kNvfp4 && ROWS && COLS &&
 // instead of 124), and patches of 8 x 8 that read the inputs once per result 140.
 //
 // Bound by instructions (five quantisations an element: 55 % of the ALU's peak): 2048 x 11008 silu
-// 75 / 91 us (mxfp4 / nvfp4; 195 MB, 2.6 TB/s), gelu 119 / 142 us.
+// 76 / 93 us (mxfp4 / nvfp4; 195 MB, 2.6 TB/s), gelu 119 / 144, tanh gelu 99 / 118; 2048 x 11007 silu
+// 136 / 153 (rows that do not start on eight bytes are read by words).
 //
 // du and dut have a factor each. Elements that saturate are cut off by the larger one (see
 // quantize_patch), which is enough for the other as long as their quotient stays an fp32 number.
@@ -663,7 +667,8 @@ __global__ void __launch_bounds__(kTileThreads, 4)
 // A lane decodes eight columns of eight rows, four rows apart, so that a warp's stores cover 128
 // consecutive bytes (bf16) of four rows. Rows of other alignment pass through shared memory, so that
 // a warp's lanes write consecutive elements. Bound by HBM, mostly by its own stores: 4096 x 11008 to
-// bf16 20 us (5.5 TB/s), 4096 x 11007 27 us (150 with the lanes' own eight elements one by one).
+// bf16 20 us (5.5 TB/s), to fp32 48; 4096 x 11007 27 and 48 us (150 and 185 with the lanes' own eight
+// elements one by one).
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kTileThreads)
     mx4_dequantize_kernel(int rows, int cols, const uint8_t* codes,
