@@ -1063,3 +1063,19 @@ for r, was, s in zip(runs, got, streams):
     assert all(torch.equal(a, b) for a, b in zip(was, r.out())) and int(r.st) == 0
 print("ok")
 """)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("f", [2.0 ** 100, 2.0 ** 117, 2.0 ** 125, 2.0 ** 127])
+def test_factors_near_the_largest_numbers(f, dtype):
+    """Scales of up to 2688 f in fp32's range, subnormal reciprocals: every decision as exact arithmetic's."""
+    x = randn(70, 200, seed=4, dtype=TYPES[dtype])
+    x *= 2.0 ** 98
+    x[::2] *= 2.0 ** 25
+    x[5], x[6, 7], x[8, :16] = torch.finfo(TYPES[dtype]).max, -torch.finfo(TYPES[dtype]).max, 0
+    xd = x.cuda()
+    q, t = operand("nvfp4", 70, 200, f=f), operand("nvfp4", 200, 70, f=f)
+    t.factor = q.factor
+    mgt.mx4_quantize(xd, q, t)
+    check_bytes(q, np64(xd), f)
+    check_bytes(t, np64(xd).T, f)
