@@ -227,12 +227,13 @@ __device__ __forceinline__ float cut_off(float z, float most) {
 template <int ACT>
 __device__ __forceinline__ void gate_and_grad(float z, float& h, float& dh) {
   if constexpr (ACT == 0) {
-    // sigmoid(z) = 2^-12 / (2^-12 + 2^-12 e^-z): the special-function unit's reciprocal is zero where
+    // sigmoid(z) = 2^-7 / (2^-7 + 2^-7 e^-z): the special-function unit's reciprocal is zero where
     // its argument passes 2^126, which 1 + e^-z does at z = -87.3, where z sigmoid(z) is a normal
-    // number yet (down to -91.8); the scaled sum does at -95.7. Relative error about 2^-21 + |z| 2^-24
-    // (the exponent's product, ex2.approx, rcp.approx), far below the 2^-3 of an element. With expf
-    // and an IEEE division, within 2^-22, the backward of 2048 x 11008 took 93 us instead of 76.
-    const float s = 0x1p-12f * rcp_approx(0x1p-12f + ex2_approx(fmaf(z, -1.4426950408889634f, -12.0f)));
+    // number yet (down to -91.8); the scaled sum does at -92.2. Relative error about 2^-21 + |z| 2^-24
+    // (the exponent's product, ex2.approx, rcp.approx), far below the 2^-3 of an element; a larger shift
+    // would cost bits of the exponent near z = 0. With expf and an IEEE division, within 2^-22, the
+    // backward of 2048 x 11008 took 91 us instead of 76.
+    const float s = 0x1p-7f * rcp_approx(0x1p-7f + ex2_approx(fmaf(z, -1.4426950408889634f, -7.0f)));
     h = z * s;
     dh = s * fmaf(z, 1.0f - s, 1.0f);
   } else if constexpr (ACT == 1) {
